@@ -456,3 +456,9 @@ def la_scan_host(mode: int, q, k, v, o=None, alpha=None, beta=None, k_scale: flo
                           int(chunk_frames), _ptr(workspace), workspace.numel(), _stream(stream))
     _raise(st, "la_scan_host")
     return o
+
+
+from .token_ops import *  # noqa: E402,F401,F403  (needs the library and helpers above)
+from . import token_ops as _token_ops  # noqa: E402
+
+__all__ += _token_ops.__all__

@@ -53,7 +53,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return LIB
     nvcc = _nvcc()
     tmp = LIB + ".tmp"
-    cmd = [nvcc, *ARCH_FLAGS, *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-shared",
+    cmd = [nvcc, "--threads", "0", *ARCH_FLAGS, *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-shared",
            "-o", tmp, *sources(), *extra]
     if verbose:
         print(" ".join(cmd), flush=True)

@@ -99,6 +99,13 @@ int device_sm_count();                  // SMs of the current device (cached per
 // earlier one, never lowered); returns the CUDA error of a failure.
 cudaError_t ensure_dyn_smem(const void* kernel, int bytes);
 
+// Argument checks shared by the entry points (la_scan.cu).
+// A pointer the kernels may dereference (NULL passes): 16-byte aligned device
+// or managed memory of device `dev`.
+la_status check_ptr(const void* p, int dev);
+bool overlaps(const void* a, size_t na, const void* b, size_t nb);
+la_status check_device(int* dev_out);    // the current device is an sm_100
+
 // Launchers (host side), each returns cudaGetLastError() of its launches.
 cudaError_t launch_simt(const ScanArgs& a, cudaStream_t st);
 int simt_kernel_count(const ScanArgs& a);

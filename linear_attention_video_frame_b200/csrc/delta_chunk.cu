@@ -1,0 +1,543 @@
+// Gated delta rule in chunks of 64 tokens on tensor cores.
+//
+// Within a chunk that starts from state S0, with G_i the sum of log_alpha up
+// to token i, gamma_i = exp(G_i), E_ij = exp(G_i - G_j), B = diag(beta), every
+// token writes a rank-one term kh_i u_i^T with
+//     (I + B N) U = B (V - gamma o (Kh S0)),   N_ij = E_ij kh_i . kh_j  (i > j).
+// Let L = N (I + B N)^-1 = N - N B L (strictly lower triangular).  Then
+//     Y = V - gamma o (Kh S0),   Z = Y - L (B Y),   U = B Z,
+//     O = gamma o (Qh S0) + P U,                P_ij = E_ij qh_i . kh_j (i >= j),
+//     S = gamma_63 S0 + Kh^T (exp(G_63 - G) o U).
+// L and P do not depend on the state: delta_prep_kernel forms them for all
+// chunks at once; delta_chain_kernel walks the chunks of a head.
+#include "delta_tiles.cuh"
+
+namespace la {
+namespace {
+
+// ---------------------------------------------------------------------------
+// L, P and the gates of every chunk
+// ---------------------------------------------------------------------------
+template <bool F32, int DP>
+struct PrepSmem {
+    static constexpr int kTile = kChunk * DP * 2;
+    static constexpr int kPlanes = Planes<F32>::kInput;
+    static constexpr int kPitch = kChunk + 4;           // floats of a row of N
+    static constexpr int kK = 0, kQ = kPlanes * kTile, kN = 2 * kPlanes * kTile;
+    static constexpr int kBytes = kN + kChunk * kPitch * 4;
+};
+
+// A block of four warps forms one chunk of one value head.
+template <bool F32, int DP>
+__global__ void __launch_bounds__(128)
+delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
+    using Sm = PrepSmem<F32, DP>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float g_hi[kChunk], g_lo[kChunk], s_beta[kChunk];
+
+    const int chunk = blockIdx.x % chunks, head = blockIdx.x / chunks;
+    const int b = head / in.Hv, h = head % in.Hv, ratio = in.Hv / in.Hk, hk = h / ratio;
+    const int len = seq_len(in.lengths, b, in.T);
+    const int t0 = chunk * kChunk;
+    if (t0 >= len) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t base = smem_u32(smem);
+    const uint32_t sK = base + Sm::kK, sQ = base + Sm::kQ;
+    float* sN = reinterpret_cast<float*>(smem + Sm::kN);
+
+    load_rows<F32, DP>(sK, in.k, row3(in.k_stride).at(b, hk, 0), in.k_stride[2], t0, len, in.D,
+                       tid, 128);
+    load_rows<F32, DP>(sQ, in.q, row3(in.q_stride).at(b, hk, 0), in.q_stride[2], t0, len, in.D,
+                       tid, 128);
+    cp_commit();
+
+    // Running sums of log_alpha in double, kept as two floats: differences of
+    // sums far from 0 keep the accuracy of their own size.
+    float* gates = ws.gates(head, chunk);
+    if (warp == 0) {
+        const size_t at = ((size_t)b * in.Hv + h) * in.T + t0;
+        double s[2];
+        float bt[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            const bool on = t0 + t < len;
+            const float g = on ? in.log_alpha[at + t] : 0.f;
+            s[i] = g < kLogAlphaMin ? kLogAlphaMin : g;         // keeps NaN
+            bt[i] = on ? in.beta[at + t] : 0.f;
+        }
+        s[1] += s[0];
+        double run = s[1];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const double y = __shfl_up_sync(~0u, run, d);
+            if (lane >= d) run += y;
+        }
+        const double before = run - s[1];
+        s[0] += before;
+        s[1] = run;
+        const double last = __shfl_sync(~0u, run, 31);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            g_hi[t] = (float)s[i];
+            g_lo[t] = (float)(s[i] - (double)g_hi[t]);
+            s_beta[t] = bt[i];
+            gates[t] = expf((float)s[i]);
+            gates[kChunk + t] = expf((float)(last - s[i]));
+            gates[2 * kChunk + t] = bt[i];
+            gates[3 * kChunk + t] = g_hi[t];
+            gates[4 * kChunk + t] = g_lo[t];
+        }
+    }
+    cp_wait<0>();
+    __syncthreads();
+
+    if (F32 && h % ratio == 0) {      // the planes of k and q that the chains load
+        unsigned char* out = ws.planes(b * in.Hk + hk, chunk);
+        for (int i = tid; i < 2 * Sm::kPlanes * Sm::kTile / 16; i += 128)
+            reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(smem)[i];
+    }
+
+    // Warp w: rows 16 w .. 16 w + 15 of Kh Kh^T and Qh Kh^T, up to the diagonal.
+    Acc kk[8], qk[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        kk[i].zero();
+        qk[i].zero();
+    }
+    constexpr int CH = DP / 8, NI = Sm::kPlanes, NP = Planes<F32>::kSplit;
+#pragma unroll 1
+    for (int ks = 0; ks < DP / 16; ++ks) {
+        uint32_t ak[NI][4], aq[NI][4];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            ldsm4(ak[i], at_rows<CH>(sK + i * Sm::kTile, warp * 16, 2 * ks, lane));
+            ldsm4(aq[i], at_rows<CH>(sQ + i * Sm::kTile, warp * 16, 2 * ks, lane));
+        }
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+            if (np > warp) break;
+            uint32_t bk[NI][4];
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+                ldsm4(bk[j], at_cols<CH>(sK + j * Sm::kTile, np * 16, 2 * ks, lane));
+            product_planes<NI, NI, NI>(kk + 2 * np, ak, bk);
+            product_planes<NI, NI, NI>(qk + 2 * np, aq, bk);
+        }
+    }
+    const int g = lane >> 2, tq = lane & 3;
+    const float k2 = in.k_scale * in.k_scale, qk_scale = in.k_scale * in.q_scale;
+    __nv_bfloat16* pOut = ws.P(head, chunk);
+    __nv_bfloat16* lOut = ws.L(head, chunk);
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+        if (nt >= 2 * (warp + 1)) break;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int i = warp * 16 + g + 8 * r, j = nt * 8 + 2 * tq;
+            float n[2], p[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                // masked places are selected away, never multiplied by 0
+                const float E = expf((g_hi[i] - g_hi[j + e]) + (g_lo[i] - g_lo[j + e]));
+                n[e] = i > j + e ? k2 * E * kk[nt][2 * r + e] : 0.f;
+                p[e] = i >= j + e ? qk_scale * E * qk[nt][2 * r + e] : 0.f;
+            }
+            *reinterpret_cast<float2*>(sN + i * Sm::kPitch + j) = make_float2(n[0], n[1]);
+            uint32_t w[NP];
+            split_bf16<NP>(p[0], p[1], w);
+#pragma unroll
+            for (int e = 0; e < NP; ++e)
+                *reinterpret_cast<uint32_t*>(pOut + (e * kChunk + i) * kChunk + j) = w[e];
+        }
+    }
+    __syncthreads();
+
+    // L = N - N B L by forward substitution, a column a thread.  Rows up to the
+    // end of a row's 16-block are in sN; what lies above the diagonal is 0.
+    if (tid < kChunk) {
+        float x[kChunk];              // beta_j L_j,tid
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < i; j += 4) {
+                const float4 nr = *reinterpret_cast<const float4*>(sN + i * Sm::kPitch + j);
+                const float nv[4] = {nr.x, nr.y, nr.z, nr.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (j + e < i) s[e] += nv[e] * x[j + e];
+            }
+            float l = 0.f;
+            if (i > tid) l = sN[i * Sm::kPitch + tid] - ((s[0] + s[1]) + (s[2] + s[3]));
+            x[i] = s_beta[i] * l;
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                const __nv_bfloat16 w = __float2bfloat16_rn(l);
+                lOut[(e * kChunk + i) * kChunk + tid] = w;
+                l -= __bfloat162float(w);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The chain over a head's chunks
+// ---------------------------------------------------------------------------
+// The columns of the state evolve independently, so a warp takes 16 of them
+// and keeps S^T (16 value columns x key rows) as float32 product tiles in
+// registers.  Everything is computed transposed: S^T is the a operand of
+// (Kh S)^T = S^T Kh^T, whose result tiles are, rounded, the a operands of the
+// products with L^T and P^T, and U^T in turn that of the update of S^T by Kh.
+// No intermediate leaves registers; shared memory holds only the chunk's K, Q,
+// L, P and V tiles, which the block's warps share.
+//
+// The chain's length, not its bytes, bounds it: a chunk costs a warp about 500
+// products of 8 cycles each.  KS warps therefore share a slice's key rows (each
+// holds DP / KS of them): their partial sums of Kh S and Qh S meet in shared
+// memory, the middle part is computed by each, the outputs are split between
+// them by token.
+template <bool F32, int DP, int KS, int SL, int STAGES, bool STATES>
+struct ChainSmem {
+    static constexpr int kTile = kChunk * DP * 2;                 // a plane of K or Q
+    static constexpr int kPlanes = Planes<F32>::kInput, kSplit = Planes<F32>::kSplit;
+    static constexpr int kLP = kChunk * kChunk * 2;               // a plane of L or P
+    static constexpr int kV = ValueTile<F32, SL>::kBytes;
+    static constexpr int kGates = 3 * kChunk * 4;
+    // offsets in a stage
+    static constexpr int oK = 0, oL = oK + kPlanes * kTile, oV = oL + kSplit * kLP,
+                         oGates = oV + kV, oQ = oGates + kGates,
+                         oP = oQ + (STATES ? 0 : kPlanes * kTile),
+                         kStage = oP + (STATES ? 0 : kSplit * kLP);
+    static constexpr int oExchange = STAGES * kStage;
+    // per warp: partial sums, 8 tiles of 512 bytes (twice with outputs)
+    static constexpr int kExchange = KS > 1 ? KS * SL * 8 * 512 * (STATES ? 1 : 2) : 0;
+    static constexpr int oOut = oExchange + kExchange;
+    static constexpr int kOut = KS * SL * (STATES ? kChunk * 32 : (kChunk / KS) * 32);
+    static constexpr int kBytes = oOut + kOut;
+};
+
+// STATES: instead of outputs, the starting state of every chunk and the final
+// one (as split S^T images) and Z (split) are written, for the backward pass.
+template <bool F32, int DP, int KS, int SL, int STAGES, bool STATES>
+__global__ void __launch_bounds__(32 * KS * SL)
+delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) {
+    using Sm = ChainSmem<F32, DP, KS, SL, STAGES, STATES>;
+    constexpr int THREADS = 32 * KS * SL;
+    constexpr int CH = DP / 8;            // 16-byte pieces of a K row
+    constexpr int DK = DP / KS;           // key rows of a warp
+    constexpr int NT = DK / 8;            // tiles of S^T in a warp
+    constexpr int NP = Planes<F32>::kSplit, NI = Planes<F32>::kInput;
+    extern __shared__ __align__(128) unsigned char smem[];
+    const uint32_t base = smem_u32(smem);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int slice = warp / KS, part = warp % KS;
+    const int g = lane >> 2, tq = lane & 3;
+    const int head = blockIdx.x, b = head / in.Hv, h = head % in.Hv, hk = h / (in.Hv / in.Hk);
+    const int D = in.D;
+    const int vb = blockIdx.y * SL * 16;      // first value column of the block
+    const int v0 = vb + slice * 16;           // of the warp
+    const bool live = v0 < D;                 // D is a multiple of 16
+    const int k0 = part * DK;
+    const int len = seq_len(in.lengths, b, in.T);
+    const int nc = (len + kChunk - 1) / kChunk;
+
+    float S[NT][4];
+    {
+        const float* s_in = in.state_in ? in.state_in + (size_t)head * D * D : nullptr;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int dk = k0 + nt * 8 + 2 * tq + (e & 1), v = v0 + g + 8 * (e >> 1);
+                S[nt][e] = s_in && live && dk < D ? s_in[(size_t)dk * D + v] : 0.f;
+            }
+    }
+
+    auto load = [&](int c, int stage) {
+        const uint32_t st = base + stage * Sm::kStage;
+        const int t0 = c * kChunk;
+        if constexpr (F32) {
+            const unsigned char* planes = ws.planes(b * in.Hk + hk, c);
+            copy_bytes(st + Sm::oK, planes, NI * Sm::kTile, tid, THREADS);
+            if constexpr (!STATES)
+                copy_bytes(st + Sm::oQ, planes + NI * Sm::kTile, NI * Sm::kTile, tid, THREADS);
+        } else {
+            load_rows<false, DP>(st + Sm::oK, in.k, row3(in.k_stride).at(b, hk, 0),
+                                 in.k_stride[2], t0, len, D, tid, THREADS);
+            if constexpr (!STATES)
+                load_rows<false, DP>(st + Sm::oQ, in.q, row3(in.q_stride).at(b, hk, 0),
+                                     in.q_stride[2], t0, len, D, tid, THREADS);
+        }
+        load_values<F32, SL>(st + Sm::oV, in.v, row3(in.v_stride).at(b, h, 0), in.v_stride[2], vb,
+                             t0, len, D, tid, THREADS);
+        load_triangle<NP>(st + Sm::oL, ws.L(head, c), tid, THREADS);
+        if constexpr (!STATES) load_triangle<NP>(st + Sm::oP, ws.P(head, c), tid, THREADS);
+        copy_bytes(st + Sm::oGates, ws.gates(head, c), Sm::kGates, tid, THREADS);
+        cp_commit();
+    };
+
+    if (STAGES > 1 && nc > 0) load(0, 0);
+    for (int c = 0; c < nc; ++c) {
+        const int stage = STAGES > 1 ? c & 1 : 0;
+        if (STAGES > 1) {
+            cp_wait<0>();
+            __syncthreads();        // the chunk has landed; the other stage is free
+            if (c + 1 < nc) load(c + 1, stage ^ 1);
+        } else {
+            __syncthreads();        // the stage is free
+            load(c, 0);
+            cp_wait<0>();
+            __syncthreads();
+        }
+        const uint32_t st = base + stage * Sm::kStage;
+        const float* gates = reinterpret_cast<const float*>(smem + stage * Sm::kStage + Sm::oGates);
+
+        if constexpr (STATES)
+            if (live) store_image<NP>(ws.states(head, c), S, v0, k0, DP, D, lane);
+
+        // (Kh S0)^T and (Qh S0)^T, this warp's key rows
+        float M[8][4], O[8][4];
+        Acc m[8], q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            m[i].zero();
+            q[i].zero();
+        }
+#pragma unroll
+        for (int ks = 0; ks < DK / 16; ++ks) {
+            uint32_t a[NP][4];
+            split_tiles<NP>(S[2 * ks], S[2 * ks + 1], a);
+            const int piece = (k0 >> 3) + 2 * ks;
+#pragma unroll
+            for (int np = 0; np < 4; ++np) {
+                product_cols<NP, NP, NI, CH>(m + 2 * np, a, st + Sm::oK, Sm::kTile, np * 16,
+                                             piece, lane);
+                if constexpr (!STATES)
+                    product_cols<NP, NP, NI, CH>(q + 2 * np, a, st + Sm::oQ, Sm::kTile,
+                                                 np * 16, piece, lane);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                M[i][e] = m[i][e];
+                O[i][e] = q[i][e];
+            }
+        if constexpr (KS > 1) {
+            float4* ex = reinterpret_cast<float4*>(smem + Sm::oExchange) + slice * KS * 256;
+            float4* exo = ex + KS * SL * 256;
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                ex[(part * 8 + nt) * 32 + lane] = make_float4(M[nt][0], M[nt][1], M[nt][2], M[nt][3]);
+                if constexpr (!STATES)
+                    exo[(part * 8 + nt) * 32 + lane] =
+                        make_float4(O[nt][0], O[nt][1], O[nt][2], O[nt][3]);
+            }
+            group_sync(1 + slice, 32 * KS);
+            // every warp adds the parts in the same order
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                sum_parts<KS>(M[nt], ex, nt, lane);
+                if constexpr (!STATES)
+                    if (nt / (8 / KS) == part) sum_parts<KS>(O[nt], exo, nt, lane);
+            }
+        }
+
+        // Y = V - gamma o (Kh S0), X = B Y (split), Z = Y - L X
+        uint32_t x[4][NP][4];
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+            float V[2][4];
+            load_v<F32, SL>(V, smem + stage * Sm::kStage + Sm::oV, st + Sm::oV,
+                            np * 16, slice, lane);
+            float X[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int nt = 2 * np + j;
+                const float2 ga = *reinterpret_cast<const float2*>(gates + nt * 8 + 2 * tq);
+                const float2 be =
+                    *reinterpret_cast<const float2*>(gates + 2 * kChunk + nt * 8 + 2 * tq);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    M[nt][e] = V[j][e] - in.k_scale * ((e & 1) ? ga.y : ga.x) * M[nt][e];
+                    X[j][e] = ((e & 1) ? be.y : be.x) * M[nt][e];
+                }
+            }
+            split_tiles<NP>(X[0], X[1], x[np]);
+        }
+#pragma unroll
+        for (int ip = 0; ip < 4; ++ip) {          // tokens 16 ip .. 16 ip + 15
+            Acc C[2];
+            C[0].zero();
+            C[1].zero();
+#pragma unroll
+            for (int jp = 0; jp <= ip; ++jp)
+                product_cols<NP, NP, NP, 8>(C, x[jp], st + Sm::oL, Sm::kLP, ip * 16, 2 * jp, lane);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) M[2 * ip + j][e] -= C[j][e];
+        }
+        if constexpr (STATES) {
+            if (live && part == 0)
+                store_rows<NP>(ws.Z(head, c), M, smem + Sm::oOut + warp * kChunk * 32, v0, DP, lane);
+        }
+
+        // U = B Z; W = exp(G_63 - G) o U for the update
+        uint32_t u[4][NP][4], w[4][NP][4];
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+            float U[2][4], W[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int nt = 2 * np + j;
+                const float2 be =
+                    *reinterpret_cast<const float2*>(gates + 2 * kChunk + nt * 8 + 2 * tq);
+                const float2 ta =
+                    *reinterpret_cast<const float2*>(gates + kChunk + nt * 8 + 2 * tq);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    U[j][e] = ((e & 1) ? be.y : be.x) * M[nt][e];
+                    W[j][e] = in.k_scale * ((e & 1) ? ta.y : ta.x) * U[j][e];
+                }
+            }
+            if constexpr (!STATES) split_tiles<NP>(U[0], U[1], u[np]);
+            split_tiles<NP>(W[0], W[1], w[np]);
+        }
+
+        // S^T <- gamma_63 S^T + W^T Kh, this warp's key rows
+        const float gc = gates[kChunk - 1];
+#pragma unroll
+        for (int np = 0; np < NT / 2; ++np) {
+            Acc C[2];
+            C[0].zero();
+            C[1].zero();
+#pragma unroll
+            for (int ts = 0; ts < 4; ++ts)
+                product_rows<NP, NP, NI, CH>(C, w[ts], st + Sm::oK, Sm::kTile, ts * 16,
+                                             (k0 >> 3) + 2 * np, lane);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                S[2 * np][e] = gc * S[2 * np][e] + C[0][e];
+                S[2 * np + 1][e] = gc * S[2 * np + 1][e] + C[1][e];
+            }
+        }
+
+        // O^T = gamma o (Qh S0)^T + U^T P^T, this warp's tokens
+        if constexpr (!STATES) {
+#pragma unroll
+            for (int ip = 0; ip < 4; ++ip) {
+                if (ip / (4 / KS) != part) continue;
+                Acc C[2];
+                C[0].zero();
+                C[1].zero();
+#pragma unroll
+                for (int jp = 0; jp <= ip; ++jp)
+                    product_cols<NP, NP, NP, 8>(C, u[jp], st + Sm::oP, Sm::kLP, ip * 16, 2 * jp,
+                                                lane);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int nt = 2 * ip + j;
+                    const float2 ga = *reinterpret_cast<const float2*>(gates + nt * 8 + 2 * tq);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        O[nt][e] = in.q_scale * ((e & 1) ? ga.y : ga.x) * O[nt][e] + C[j][e];
+                }
+            }
+            if (live)
+                store_out<F32, KS>(o, os.at(b, h, c * kChunk), os.t, O,
+                                   smem + Sm::oOut + warp * (kChunk / KS) * 32, part, v0,
+                                   len - c * kChunk, lane);
+        }
+    }
+    if constexpr (STATES) {
+        if (live) store_image<NP>(ws.states(head, nc), S, v0, k0, DP, D, lane);
+    }
+    if (state_out && live) {
+        float* s_out = state_out + (size_t)head * D * D;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int dk = k0 + nt * 8 + 2 * tq + (e & 1), v = v0 + g + 8 * (e >> 1);
+                if (dk < D) s_out[(size_t)dk * D + v] = S[nt][e];
+            }
+    }
+}
+
+template <bool F32, int DP>
+cudaError_t prep(const la_delta& in, const DeltaWs& ws, cudaStream_t st) {
+    using Sm = PrepSmem<F32, DP>;
+    const int chunks = (in.T + kChunk - 1) / kChunk;
+    auto* kernel = delta_prep_kernel<F32, DP>;
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), Sm::kBytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)(in.B * in.Hv) * (unsigned)chunks, 128, Sm::kBytes, st>>>(in, ws, chunks);
+    return cudaGetLastError();
+}
+
+template <bool F32, int DP, int KS, int SL, bool STATES>
+cudaError_t chain(const la_delta& in, const DeltaWs& ws, void* o, Row3 os, float* state_out,
+                  cudaStream_t st) {
+    // two stages where they fit (float32 planes of a 128-row state do not)
+    constexpr int STAGES = ChainSmem<F32, DP, KS, SL, 2, STATES>::kBytes <= 227 * 1024 ? 2 : 1;
+    using Sm = ChainSmem<F32, DP, KS, SL, STAGES, STATES>;
+    static_assert(Sm::kBytes <= 227 * 1024, "shared memory of a block");
+    auto* kernel = delta_chain_kernel<F32, DP, KS, SL, STAGES, STATES>;
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), Sm::kBytes);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(in.B * in.Hv, (in.D + 16 * SL - 1) / (16 * SL));
+    kernel<<<grid, 32 * KS * SL, Sm::kBytes, st>>>(in, ws, o, os, state_out);
+    return cudaGetLastError();
+}
+
+template <bool F32, int DP>
+cudaError_t forward(const la_delta& in, const DeltaWs& ws, void* o, Row3 os, float* state_out,
+                    cudaStream_t st) {
+    cudaError_t e = prep<F32, DP>(in, ws, st);
+    if (e != cudaSuccess) return e;
+    return chain<F32, DP, 4, 1, false>(in, ws, o, os, state_out, st);
+}
+
+template <bool F32, int DP>
+cudaError_t states(const la_delta& in, const DeltaWs& ws, cudaStream_t st) {
+    cudaError_t e = prep<F32, DP>(in, ws, st);
+    if (e != cudaSuccess) return e;
+    return chain<F32, DP, 4, 1, true>(in, ws, nullptr, Row3{0, 0, 0}, nullptr, st);
+}
+
+}  // namespace
+
+bool delta_chunked(int backward, int T, int D) {
+    return backward || (T >= kChunk && D <= 128);
+}
+
+size_t delta_workspace_bytes(int backward, int dt, int B, int Hk, int Hv, int T, int D) {
+    if (!delta_chunked(backward, T, D)) return 256;
+    return DeltaWs::layout(nullptr, backward, dt, B, Hk, Hv, T, D).bytes;
+}
+
+int delta_kernel_count(int backward) { return backward ? 4 : 2; }
+
+cudaError_t launch_delta_chunked(const la_delta& in, void* o, const long long o_stride[3],
+                                 float* state_out, void* ws_mem, cudaStream_t st) {
+    const DeltaWs ws = DeltaWs::layout(ws_mem, 0, in.dt, in.B, in.Hk, in.Hv, in.T, in.D);
+    const Row3 os = row3(o_stride);
+    if (in.dt == LA_BF16)
+        return in.D <= 64 ? forward<false, 64>(in, ws, o, os, state_out, st)
+                          : forward<false, 128>(in, ws, o, os, state_out, st);
+    return in.D <= 64 ? forward<true, 64>(in, ws, o, os, state_out, st)
+                      : forward<true, 128>(in, ws, o, os, state_out, st);
+}
+
+cudaError_t launch_delta_states(const la_delta& in, const DeltaWs& ws, cudaStream_t st) {
+    if (in.dt == LA_BF16)
+        return in.D <= 64 ? states<false, 64>(in, ws, st) : states<false, 128>(in, ws, st);
+    return in.D <= 64 ? states<true, 64>(in, ws, st) : states<true, 128>(in, ws, st);
+}
+
+}  // namespace la

@@ -1,0 +1,348 @@
+// Workspace and tile helpers of the chunked gated delta rule.
+#pragma once
+
+#include "mma.cuh"
+#include "token.cuh"
+
+namespace la {
+
+// Planes that a computed operand is split into (float32 values as sums of
+// bf16, see mma.cuh), and planes of the inputs.  bf16 inputs are exact in one
+// plane.  Computed values take three (2^-27): states and gate gradients leave in
+// float32, where two planes would show (3e-6 of the state in place of 1e-7).
+template <bool F32> struct Planes {
+    static constexpr int kSplit = 3;
+    static constexpr int kInput = F32 ? 3 : 1;
+};
+
+// Per token: exp(G), exp(G_63 - G), beta, and G as the sum of two floats.
+constexpr int kGateRows = 5;
+
+// What the kernels of a call hand to one another.  L and P are [64][64] bf16
+// planes; blocks of 16 above the diagonal are not written.  States are images
+// [value column][key row] of DP columns in planes; Z and dX are rows
+// [token][value column] of DP columns in planes.
+struct DeltaWs {
+    unsigned char *gates_, *L_, *P_, *planes_, *states_, *dstates_, *Z_, *dX_;
+    int chunks;          // per head
+    int DP, D, NP;
+    size_t bytes;
+
+    static DeltaWs layout(void* mem, int backward, int dt, int B, int Hk, int Hv, int T, int D) {
+        DeltaWs w{};
+        w.chunks = (T + kChunk - 1) / kChunk;
+        w.DP = D <= 64 ? 64 : 128;
+        w.D = D;
+        w.NP = dt == LA_F32 ? Planes<true>::kSplit : Planes<false>::kSplit;
+        const size_t n = (size_t)B * Hv * w.chunks, nk = (size_t)B * Hk * w.chunks;
+        size_t at = kWsHeaderBytes;
+        unsigned char* p = static_cast<unsigned char*>(mem);
+        auto take = [&](size_t size) {
+            unsigned char* r = p + at;
+            at = align_up(at + size, 256);
+            return r;
+        };
+        w.gates_ = take(n * kGateRows * kChunk * 4);
+        w.L_ = take(n * w.NP * 2 * kChunk * kChunk);
+        w.P_ = take(n * w.NP * 2 * kChunk * kChunk);
+        w.planes_ = take(dt == LA_F32 ? nk * 2 * w.NP * w.plane_bytes() : 0);
+        if (backward) {
+            w.states_ = take((size_t)B * Hv * (w.chunks + 1) * w.image_bytes());
+            w.dstates_ = take(n * w.image_bytes());
+            w.Z_ = take(n * w.NP * w.plane_bytes());
+            w.dX_ = take(n * w.NP * w.plane_bytes());
+        }
+        w.bytes = at;
+        return w;
+    }
+    __host__ __device__ size_t plane_bytes() const { return (size_t)kChunk * DP * 2; }
+    __host__ __device__ size_t image_bytes() const { return (size_t)D * DP * 2 * NP; }
+    __device__ size_t at(int head, int c) const { return (size_t)head * chunks + c; }
+    __device__ float* gates(int head, int c) const {
+        return reinterpret_cast<float*>(gates_) + at(head, c) * kGateRows * kChunk;
+    }
+    __device__ __nv_bfloat16* L(int head, int c) const {
+        return reinterpret_cast<__nv_bfloat16*>(L_) + at(head, c) * NP * kChunk * kChunk;
+    }
+    __device__ __nv_bfloat16* P(int head, int c) const {
+        return reinterpret_cast<__nv_bfloat16*>(P_) + at(head, c) * NP * kChunk * kChunk;
+    }
+    // float32 inputs: the planes of K, then of Q, as shared-memory tiles
+    __device__ unsigned char* planes(int khead, int c) const {
+        return planes_ + ((size_t)khead * chunks + c) * 2 * NP * plane_bytes();
+    }
+    __device__ __nv_bfloat16* states(int head, int c) const {       // c = 0 .. chunks
+        return reinterpret_cast<__nv_bfloat16*>(
+            states_ + ((size_t)head * (chunks + 1) + c) * image_bytes());
+    }
+    __device__ __nv_bfloat16* dstates(int head, int c) const {
+        return reinterpret_cast<__nv_bfloat16*>(dstates_ + at(head, c) * image_bytes());
+    }
+    __device__ __nv_bfloat16* Z(int head, int c) const {
+        return reinterpret_cast<__nv_bfloat16*>(Z_ + at(head, c) * NP * plane_bytes());
+    }
+    __device__ __nv_bfloat16* dX(int head, int c) const {
+        return reinterpret_cast<__nv_bfloat16*>(dX_ + at(head, c) * NP * plane_bytes());
+    }
+};
+
+// prep and forward chain of the backward pass (delta_chunk.cu)
+cudaError_t launch_delta_states(const la_delta& in, const DeltaWs& ws, cudaStream_t st);
+
+#ifdef __CUDACC__
+
+// Rows t0 .. t0 + 63 of a [T, D] matrix as bf16 tiles of DP columns: one plane
+// by asynchronous copies (bf16), or split planes (float32).  Rows from
+// `len` on and columns from D on are 0 and not read.
+template <bool F32, int DP>
+__device__ __forceinline__ void load_rows(uint32_t dst, const void* src, long long offset,
+                                          long long stride, int t0, int len, int D, int tid,
+                                          int threads) {
+    constexpr int CH = DP / 8;
+    for (int i = tid; i < kChunk * CH; i += threads) {
+        const int r = i / CH, c = i % CH;
+        const bool on = t0 + r < len && c * 8 < D;
+        const long long at = offset + (t0 + r) * stride + c * 8;
+        if constexpr (F32) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+            if (on) {
+                const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
+                x = p[0];
+                y = p[1];
+            }
+            constexpr int NP = Planes<true>::kInput;
+            const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            uint32_t w[4][NP];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split_bf16<NP>(f[2 * e], f[2 * e + 1], w[e]);
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};"
+                             :: "r"(dst + j * kChunk * DP * 2 + tile_at<CH>(r, c)), "r"(w[0][j]),
+                                "r"(w[1][j]), "r"(w[2][j]), "r"(w[3][j]) : "memory");
+        } else {
+            const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(src);
+            cp16(dst + tile_at<CH>(r, c), on ? p + at : p, on);
+        }
+    }
+}
+
+// A run of bytes as it lies (a multiple of 16).
+__device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, int bytes, int tid,
+                                           int threads) {
+    for (int i = tid; i < bytes / 16; i += threads)
+        cp16(dst + i * 16, static_cast<const unsigned char*>(src) + i * 16, true);
+}
+
+// NP planes of a [64][64] lower triangle, whole 16-blocks up to the diagonal.
+template <int NP>
+__device__ __forceinline__ void load_triangle(uint32_t dst, const __nv_bfloat16* src, int tid,
+                                              int threads) {
+    for (int i = tid; i < NP * kChunk * 8; i += threads) {
+        const int r = (i >> 3) & 63, c = i & 7;
+        if (c < 2 * ((r >> 4) + 1))
+            cp16(dst + (i >> 9) * (kChunk * kChunk * 2) + tile_at<8>(r, c), src + i * 8, true);
+    }
+}
+
+// A product tile in two sums: the leading planes' product, and the products
+// with a lower plane.  The tensor core rounds its sums towards zero, so a sum
+// loses up to half a last place for each product added to it: few are added to
+// the large one, and none to a value that lives longer than its chunk (adding
+// them to the state itself cost 5e-6 over 16 chunks).
+struct Acc {
+    float hi[4], lo[4];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) hi[e] = lo[e] = 0.f;
+    }
+    __device__ __forceinline__ float operator[](int e) const { return hi[e] + lo[e]; }
+};
+
+// c[0], c[1] += a b for two tiles of eight b rows each (k along the rows of the
+// tile); a in NA planes, b in NB planes `plane` bytes apart, pairs whose
+// indices add up to less than NP.
+template <int NP, int NA, int NB>
+__device__ __forceinline__ void product_planes(Acc* c, const uint32_t (&a)[NA][4],
+                                               const uint32_t (&b)[NB][4]) {
+#pragma unroll
+    for (int s = NP - 1; s >= 0; --s)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const int i = s - j;
+            if (i < 0 || i >= NA) continue;
+            mma_bf16(s ? c[0].lo : c[0].hi, a[i], b[j][0], b[j][1]);
+            mma_bf16(s ? c[1].lo : c[1].hi, a[i], b[j][2], b[j][3]);
+        }
+}
+template <int NP, int NA, int NB, int CH>
+__device__ __forceinline__ void product_cols(Acc* c, const uint32_t (&a)[NA][4], uint32_t tile,
+                                             int plane, int row, int piece, int lane) {
+    uint32_t b[NB][4];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) ldsm4(b[j], at_cols<CH>(tile + j * plane, row, piece, lane));
+    product_planes<NP, NA, NB>(c, a, b);
+}
+// The same with k down the rows of the tile; two tiles of eight columns.
+template <int NP, int NA, int NB, int CH>
+__device__ __forceinline__ void product_rows(Acc* c, const uint32_t (&a)[NA][4], uint32_t tile,
+                                             int plane, int row, int piece, int lane) {
+    uint32_t b[NB][4];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) ldsm4_t(b[j], at_rows<CH>(tile + j * plane, row, piece, lane));
+    product_planes<NP, NA, NB>(c, a, b);
+}
+
+__device__ __forceinline__ void group_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+
+template <int KS>
+__device__ __forceinline__ void sum_parts(float (&m)[4], const float4* ex, int nt, int lane) {
+    float4 s = ex[nt * 32 + lane];
+#pragma unroll
+    for (int p = 1; p < KS; ++p) {
+        const float4 x = ex[(p * 8 + nt) * 32 + lane];
+        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    m[0] = s.x; m[1] = s.y; m[2] = s.z; m[3] = s.w;
+}
+
+// The block's value columns vb .. vb + 16 SL - 1 of a chunk's rows: bf16 as a
+// permuted tile, float32 as rows of SL * 16 + 4 floats.  0 where there is none.
+template <bool F32, int SL>
+struct ValueTile {
+    static constexpr int kPitch = F32 ? SL * 16 + 4 : SL * 16;   // elements
+    static constexpr int kBytes = kChunk * kPitch * (F32 ? 4 : 2);
+};
+template <bool F32, int SL>
+__device__ __forceinline__ void load_values(uint32_t dst, const void* src, long long offset,
+                                            long long stride, int vb, int t0, int len, int D,
+                                            int tid, int threads) {
+    constexpr int N = F32 ? 4 : 8, CH = SL * 16 / N;
+    for (int i = tid; i < kChunk * CH; i += threads) {
+        const int r = i / CH, c = i % CH;
+        const bool on = t0 + r < len && vb + c * N < D;
+        const long long at = on ? offset + (t0 + r) * stride + vb + c * N : 0;
+        if constexpr (F32)
+            cp16(dst + (r * ValueTile<true, SL>::kPitch + c * 4) * 4,
+                 static_cast<const float*>(src) + at, on);
+        else
+            cp16(dst + tile_at<SL * 2>(r, c), static_cast<const __nv_bfloat16*>(src) + at, on);
+    }
+}
+
+// 16 tokens of a slice's 16 value columns, transposed into two product tiles.
+template <bool F32, int SL>
+__device__ __forceinline__ void load_v(float (&V)[2][4], const unsigned char* ptr, uint32_t addr,
+                                       int row, int slice, int lane) {
+    if constexpr (F32) {
+        constexpr int pitch = ValueTile<true, SL>::kPitch;
+        const float* v = reinterpret_cast<const float*>(ptr) + slice * 16 + (lane >> 2);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                V[j][e] = v[(row + j * 8 + 2 * (lane & 3) + (e & 1)) * pitch + 8 * (e >> 1)];
+    } else {
+        uint32_t r[4];      // (columns 0-7, tokens 0-7) (0-7, 8-15) (8-15, 0-7) (8-15, 8-15)
+        ldsm4_t(r, at_rows<SL * 2>(addr, row, slice * 2, lane));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            V[j][0] = __uint_as_float(r[j] << 16);
+            V[j][1] = __uint_as_float(r[j] & 0xffff0000u);
+            V[j][2] = __uint_as_float(r[2 + j] << 16);
+            V[j][3] = __uint_as_float(r[2 + j] & 0xffff0000u);
+        }
+    }
+}
+
+// S^T tiles of a warp (16 value columns, key rows from k0) into an image.
+template <int NP, int NT>
+__device__ __forceinline__ void store_image(__nv_bfloat16* image, const float (&S)[NT][4], int v0,
+                                            int k0, int DP, int D, int lane) {
+    __nv_bfloat16* p = image + (size_t)(v0 + (lane >> 2)) * DP + k0 + 2 * (lane & 3);
+    const size_t plane = (size_t)D * DP;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            uint32_t w[NP];
+            split_bf16<NP>(S[nt][2 * r], S[nt][2 * r + 1], w);
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+                *reinterpret_cast<uint32_t*>(p + j * plane + (size_t)r * 8 * DP + nt * 8) = w[j];
+        }
+}
+
+// 64 tokens of a warp's 16 value columns (transposed tiles) as planes of rows
+// of DP columns.  `stage`: 64 x 32 bytes of the warp's own.
+template <int NP>
+__device__ __forceinline__ void store_rows(__nv_bfloat16* out, const float (&M)[8][4],
+                                           unsigned char* stage, int v0, int DP, int lane) {
+    const uint32_t sm = smem_u32(stage);
+    uint32_t w[8][2][NP];
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+        split_bf16<NP>(M[nt][0], M[nt][1], w[nt][0]);
+        split_bf16<NP>(M[nt][2], M[nt][3], w[nt][1]);
+    }
+#pragma unroll
+    for (int plane = 0; plane < NP; ++plane) {
+        __syncwarp();
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+            stsm2_t(sm + (nt * 8 + (lane & 7)) * 32 + ((lane >> 3) & 1) * 16, w[nt][0][plane],
+                    w[nt][1][plane]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = i * 32 + lane, r = at >> 1, half = at & 1;
+            *reinterpret_cast<uint4*>(out + (size_t)plane * kChunk * DP + r * DP + v0 + half * 8) =
+                *reinterpret_cast<const uint4*>(stage + at * 16);
+        }
+    }
+}
+
+// A warp's share of the chunk's outputs: tokens 64 / KS * part .., `rows` of
+// the chunk's tokens exist.  `stage`: 64 / KS x 32 bytes of the warp's own.
+template <bool F32, int KS>
+__device__ __forceinline__ void store_out(void* o, long long offset, long long stride,
+                                          const float (&O)[8][4], unsigned char* stage, int part,
+                                          int v0, int rows, int lane) {
+    constexpr int TILES = 8 / KS;
+    if constexpr (F32) {
+        float* p = static_cast<float*>(o) + offset + v0 + (lane >> 2);
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+            if (nt / TILES != part) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = nt * 8 + 2 * (lane & 3) + (e & 1);
+                if (t < rows) p[t * stride + 8 * (e >> 1)] = O[nt][e];
+            }
+        }
+    } else {
+        const uint32_t sm = smem_u32(stage);
+        __syncwarp();
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+            if (nt / TILES != part) continue;
+            stsm2_t(sm + ((nt % TILES) * 8 + (lane & 7)) * 32 + ((lane >> 3) & 1) * 16,
+                    pack_bf16(O[nt][0], O[nt][1]), pack_bf16(O[nt][2], O[nt][3]));
+        }
+        __syncwarp();
+        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(o) + offset + v0;
+#pragma unroll
+        for (int i = lane; i < TILES * 16; i += 32) {
+            const int t = part * TILES * 8 + (i >> 1);
+            if (t < rows)
+                *reinterpret_cast<uint4*>(p + t * stride + (i & 1) * 8) =
+                    *reinterpret_cast<const uint4*>(stage + i * 16);
+        }
+    }
+}
+
+#endif  // __CUDACC__
+
+}  // namespace la

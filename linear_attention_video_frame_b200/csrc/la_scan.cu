@@ -6,11 +6,8 @@
 #include "common.cuh"
 
 namespace la {
-namespace {
 
-bool shape_supported(int D) { return D >= 16 && D <= 256 && D % 16 == 0; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // A pointer the kernels may dereference: device or managed memory of the
 // current device.  NULL is accepted here (callers decide whether NULL is legal).
@@ -47,6 +44,10 @@ la_status check_device(int* dev_out) {
     *dev_out = dev;
     return LA_OK;
 }
+
+namespace {
+
+bool shape_supported(int D) { return D >= 16 && D <= 256 && D % 16 == 0; }
 
 // LA_SCAN_FORCE_SIMT=1 in the environment routes every call to the float32
 // SIMT kernel (used by tests to compare the two kernel paths).

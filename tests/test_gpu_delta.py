@@ -1,0 +1,302 @@
+"""The gated delta rule with one update per token (chunked, its backward pass,
+single tokens) against its definition in float64."""
+import pytest
+import torch
+
+import linear_attention_video_frame_b200 as la
+from token_ref import (NAMES, U, check, check_grads, delta_bound, delta_grads_ref, delta_inputs,
+                       delta_ref, to64)
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    torch.cuda.init()
+
+
+def _args(x):
+    return tuple(x[n] for n in ("q", "k", "v", "log_alpha", "beta"))
+
+
+def _kw(x):
+    return dict(k_scale=x["k_scale"], q_scale=x["q_scale"], lengths=x["lengths"])
+
+
+def _forward(x, **kw):
+    B, Hv, T, D = x["v"].shape
+    end = torch.full((B, Hv, D, D), float("nan"), device="cuda")
+    o = la.la_gated_delta_rule(*_args(x), state_in=x["state"], state_out=end, **_kw(x), **kw)
+    return o, end
+
+
+def _backward(x, **kw):
+    B, Hv, T, D = x["v"].shape
+    dstate = torch.full((B, Hv, D, D), float("nan"), device="cuda")
+    g = la.la_gated_delta_rule_backward(*_args(x), x["do"], state_in=x["state"],
+                                        dstate_out=x["dstate"], dstate_in=dstate, **_kw(x), **kw)
+    return dict(zip(NAMES, (*g, dstate)))
+
+
+def _same(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+# one token to several chunks, ends inside and at a chunk's border
+@pytest.mark.parametrize("T", [1, 2, 63, 64, 65, 127, 129, 320])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_forward_lengths(T, dtype):
+    x = delta_inputs(2, 2, 4, T, 64, dtype, seed=T, state=T % 2 == 0)
+    o, end = _forward(x)
+    ro, rs = delta_ref(**to64(x))
+    check(o, ro, delta_bound(T), "o")
+    check(end, rs, delta_bound(T), "state")
+
+
+@pytest.mark.parametrize("D", [16, 32, 48, 80, 96, 112, 128, 144, 256])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_forward_head_widths(D, dtype):
+    x = delta_inputs(1, 1, 2, 150, D, dtype, seed=D, token_major=True)
+    o, end = _forward(x)
+    ro, rs = delta_ref(**to64(x))
+    check(o, ro, delta_bound(150), "o")
+    check(end, rs, delta_bound(150), "state")
+
+
+@pytest.mark.parametrize("Hk,Hv", [(1, 1), (1, 4), (3, 6), (5, 5)])
+@pytest.mark.parametrize("lengths", [[0, 130, 64], [1, 63, 129]])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_forward_ragged(Hk, Hv, lengths, dtype):
+    x = delta_inputs(3, Hk, Hv, 130, 48, dtype, seed=Hv, lengths=lengths)
+    for b, n in enumerate(lengths):          # what lies behind a sequence does not matter
+        for name in ("q", "k", "v"):
+            x[name][b, :, n:] = float("nan")
+        for name in ("log_alpha", "beta"):
+            x[name][b, :, n:] = float("nan")
+    o = torch.full_like(x["v"], 7.0)
+    got, end = _forward(x, o=o)
+    clean = {**x, **{n: torch.nan_to_num(x[n]) for n in ("q", "k", "v", "log_alpha", "beta")}}
+    ro, rs = delta_ref(**to64(clean))
+    for b, n in enumerate(lengths):
+        if n < 130:
+            assert (o[b, :, n:] == 7.0).all(), "rows behind a sequence were written"
+        if n:
+            check(o[b:b + 1, :, :n], ro[b:b + 1, :, :n], delta_bound(130), "o")
+        else:
+            assert torch.equal(end[b], x["state"][b])
+    check(end, rs, delta_bound(130), "state")
+
+
+@pytest.mark.parametrize("T,D", [(70, 64), (200, 128), (40, 32)])
+def test_forgetting_tokens(T, D):
+    """log_alpha of -inf, of the type's lowest value and of 0; beta of 0 and 1."""
+    x = delta_inputs(1, 2, 2, T, D, seed=T)
+    x["log_alpha"][:, 0, ::7] = -float("inf")
+    x["log_alpha"][:, 1, 5::31] = torch.finfo(F32).min
+    x["log_alpha"][:, 1, 6:20] = 0.0
+    x["beta"][:, :, ::5] = 0.0
+    x["beta"][:, :, 3::5] = 1.0
+    o, end = _forward(x)
+    ro, rs = delta_ref(**to64(x))
+    check(o, ro, delta_bound(T), "o")
+    check(end, rs, delta_bound(T), "state")
+    got = _backward(x)
+    # autograd of exp at -inf is 0 * inf; at -2000 exp is 0 in float64 as well (1e-304 at -700)
+    y = {**x, "log_alpha": x["log_alpha"].clamp_min(-2000.0)}
+    check_grads(got, delta_grads_ref(y), y, 4 * delta_bound(T))
+
+
+def test_nothing_read_back_from_forgotten_state():
+    """A state of infinities before a token that forgets it."""
+    x = delta_inputs(1, 1, 1, 3, 32, seed=5)
+    x["log_alpha"][:, :, 0] = 0.0
+    a, _ = _forward(x)
+    assert torch.isfinite(a).all()
+
+
+def test_empty_call_copies_the_state():
+    x = delta_inputs(2, 1, 2, 0, 32, seed=1)
+    o, end = _forward(x)
+    assert o.shape[2] == 0 and torch.equal(end, x["state"])
+    g = _backward(x)
+    assert torch.equal(g["state"], x["dstate"])
+    x["state"] = x["dstate"] = None
+    assert (_forward(x)[1] == 0).all() and (_backward(x)["state"] == 0).all()
+
+
+@pytest.mark.parametrize("T", [64, 200])
+def test_broadcast_and_strided_inputs(T):
+    """Heads expanded from one, and rows cut from a wider projection."""
+    x = delta_inputs(2, 4, 4, T, 64, seed=3)
+    wide = torch.randn(2, T, 4 * 64 * 3, device="cuda").to(BF16)
+    x["q"] = (wide[..., :256].unflatten(-1, (4, 64)) / 8).transpose(1, 2)
+    x["v"] = wide[..., 512:].unflatten(-1, (4, 64)).transpose(1, 2)
+    x["k"] = x["k"][:, :1].expand(-1, 4, -1, -1)
+    x["do"] = x["do"][:, :, :1].expand(-1, -1, T, -1)
+    o, end = _forward(x)
+    ro, rs = delta_ref(**to64(x))
+    # q of a wide projection is not of unit length: |q| is about 1 here too (randn / 8)
+    check(o, ro, delta_bound(T), "o")
+    check(end, rs, delta_bound(T), "state")
+    plain = {n: t.contiguous() if torch.is_tensor(t) else t for n, t in x.items()}
+    assert _same(o, _forward(plain)[0])
+    a, b = _backward(x), _backward(plain)
+    assert all(_same(a[n], b[n]) for n in NAMES)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_state_in_place_and_split_calls(D):
+    """A prompt in two calls and then token by token is the prompt in one call."""
+    T, cut = 150, 140
+    x = delta_inputs(2, 2, 4, T, D, seed=9)
+    o, end = _forward(x)
+    state = x["state"].clone()
+    part = lambda t, a, b: t[:, :, a:b].contiguous()
+    o1 = la.la_gated_delta_rule(*(part(t, 0, cut) for t in _args(x)), state_in=state,
+                                state_out=state, k_scale=x["k_scale"], q_scale=x["q_scale"])
+    rest = []
+    for t in range(cut, T):
+        rest.append(la.la_gated_delta_step(*(a[:, :, t].contiguous() for a in _args(x)), state,
+                                           k_scale=x["k_scale"], q_scale=x["q_scale"]))
+    ro, rs = delta_ref(**to64(x))
+    check(torch.cat([o1, torch.stack(rest, 2)], 2), ro, delta_bound(T), "o")
+    check(state, rs, delta_bound(T) + 8 * (T - cut) * U, "state")
+    check(end, rs, delta_bound(T), "state of one call")
+
+
+@pytest.mark.parametrize("B,Hk,Hv,D", [(1, 1, 1, 16), (3, 2, 6, 80), (1, 20, 20, 128),
+                                       (64, 2, 2, 64), (2, 1, 3, 240), (33, 4, 8, 112)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_step(B, Hk, Hv, D, dtype):
+    lengths = [i % 3 for i in range(B)]      # 0 leaves a sequence alone; more than 1 is taken as 1
+    x = delta_inputs(B, Hk, Hv, 1, D, dtype, seed=D + B, lengths=lengths)
+    a = [t[:, :, 0] for t in _args(x)]
+    a[3], a[4] = a[3].contiguous(), a[4].contiguous()
+    new = torch.empty_like(x["state"])
+    o = torch.full((B, Hv, D), 7.0, dtype=dtype, device="cuda")
+    la.la_gated_delta_step(*a, x["state"], state_out=new, o=o, **_kw(x))
+    ro, rs = delta_ref(**to64(x))
+    # a token: two sums of D products, in part sums of at most 8 and their join of 32
+    bound = 2 * 48 * U
+    for b in range(B):
+        if lengths[b] == 0:
+            assert (o[b] == 7.0).all() and torch.equal(new[b], x["state"][b])
+        else:
+            check(o[b:b + 1, :, None], ro[b:b + 1], bound, "o")
+            check(new[b:b + 1], rs[b:b + 1], bound, "state")
+    inplace = x["state"].clone()
+    la.la_gated_delta_step(*a, inplace, o=o, **_kw(x))
+    assert _same(inplace, new)
+
+
+# The backward pass runs the forward's products and as many again; a gradient
+# is a sum of up to six of them.
+@pytest.mark.parametrize("T", [1, 63, 64, 65, 130, 200])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_backward_lengths(T, dtype):
+    x = delta_inputs(1, 1, 2, T, 64, dtype, seed=T, state=T % 2 == 0)
+    got, ref = _backward(x), delta_grads_ref(x)
+    check_grads(got, ref, x, 4 * delta_bound(T))
+
+
+@pytest.mark.parametrize("D", [16, 48, 80, 112, 128])
+@pytest.mark.parametrize("Hk,Hv", [(1, 1), (2, 6)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_backward_shared_heads_ragged(D, Hk, Hv, dtype):
+    lengths = [100, 0, 65]
+    x = delta_inputs(3, Hk, Hv, 100, D, dtype, seed=D, lengths=lengths, token_major=True)
+    got, ref = _backward(x), delta_grads_ref(x)
+    check_grads(got, ref, x, 4 * delta_bound(100))
+    for b, m in enumerate(lengths):
+        for n in NAMES[:5]:
+            assert (got[n][b, :, m:] == 0).all(), f"d{n} behind a sequence"
+
+
+def test_backward_against_differences():
+    """Directional derivatives of the float64 forward pass."""
+    x = delta_inputs(1, 2, 4, 90, 32, F32, seed=11)
+    got = _backward(x)
+    y = to64(x)
+    do, ds = x["do"].cpu().double(), x["dstate"].cpu().double()
+
+    def loss(z):
+        o, S = delta_ref(**z)
+        return float((o * do).sum() + (S * ds).sum())
+
+    g = torch.Generator().manual_seed(1)
+    for n in NAMES:
+        d = torch.randn(y[n].shape, generator=g, dtype=torch.float64)
+        h = 1e-4
+        plus = loss({**y, n: y[n] + h * d})
+        minus = loss({**y, n: y[n] - h * d})
+        slope = (plus - minus) / (2 * h)
+        mine = got[n].cpu().double()
+        # each element is off by at most the bound of the largest; the rest of the
+        # difference quotient is of order h^2 = 1e-8
+        room = 4 * delta_bound(90) * float(mine.abs().max()) * float(d.abs().sum())
+        assert abs(float((mine * d).sum()) - slope) <= room + 1e-5 * abs(slope), n
+
+
+def test_backward_in_place_and_without_state():
+    x = delta_inputs(2, 1, 1, 70, 64, seed=2)
+    want = _backward(x)
+    ds = x["dstate"].clone()
+    la.la_gated_delta_rule_backward(*_args(x), x["do"], state_in=x["state"], dstate_out=ds,
+                                    dstate_in=ds, **_kw(x))
+    assert _same(ds, want["state"])
+    g = la.la_gated_delta_rule_backward(*_args(x), x["do"], state_in=x["state"],
+                                        dstate_out=x["dstate"], **_kw(x))
+    assert all(_same(a, want[n]) for a, n in zip(g, NAMES))
+
+
+def test_equal_calls_give_equal_bits():
+    x = delta_inputs(2, 4, 8, 333, 128, seed=21)
+    (a, s), (b, t) = _forward(x), _forward(x)
+    assert _same(a, b) and _same(s, t)
+    g, h = _backward(x), _backward(x)
+    assert all(_same(g[n], h[n]) for n in NAMES)
+
+
+def test_graphs_on_another_stream_with_their_own_workspaces():
+    """Two captured calls of different shapes, replayed against each other."""
+    xs = [delta_inputs(1, 2, 2, 200, 64, seed=31), delta_inputs(2, 1, 2, 90, 128, seed=32)]
+    want = [(_forward(x), _backward(x)) for x in xs]
+    graphs, outs = [], []
+    for x in xs:
+        B, Hv, T, D = x["v"].shape
+        ws = [la.delta_workspace_for(bw, la.LA_BF16, B, x["q"].shape[1], Hv, T, D)
+              for bw in (False, True)]
+        st = torch.cuda.Stream()
+        g = torch.cuda.CUDAGraph()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(g, stream=st):
+            outs.append((_forward(x, workspace=ws[0], stream=st),
+                         _backward(x, workspace=ws[1], stream=st)))
+        graphs.append((g, st, ws))
+    for _ in range(3):
+        for g, st, _ in graphs:
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for (f, b), (wf, wb) in zip(outs, want):
+        assert _same(f[0], wf[0]) and _same(f[1], wf[1])
+        assert all(_same(b[n], wb[n]) for n in NAMES)
+    del graphs, g
+
+
+def test_long_sequence_offsets():
+    """Rows whose element offsets pass 31 bits (a long batch with wide strides)."""
+    T, D = 130, 64
+    stride = (1 << 31) // T // 8 * 8 + 4096
+    big = torch.empty(T * stride + D, dtype=BF16, device="cuda")
+    x = delta_inputs(1, 1, 1, T, D, seed=41)
+    rows = big.as_strided((1, 1, T, D), (0, 0, stride, 1))
+    rows.copy_(x["k"])
+    want = _forward(x)
+    got = _forward({**x, "k": rows})
+    assert _same(got[0], want[0]) and _same(got[1], want[1])
+    o = big.as_strided((1, 1, T, D), (0, 0, stride, 1), 128)
+    la.la_gated_delta_rule(*_args(x), state_in=x["state"], o=o, **_kw(x))
+    assert _same(o, want[0])
