@@ -18,20 +18,30 @@ namespace {
 // ---------------------------------------------------------------------------
 // L, P and the gates of every chunk
 // ---------------------------------------------------------------------------
+// A block of four warps forms one chunk of one value head.
+//
+// L goes by blocks of 16: the four diagonal blocks by forward substitution (a
+// column a lane, 120 steps), then block column c by warp c from the top,
+//     R = N_rc - sum_j N_rj (B L_jc),   L_rc = R - L_rr (B R),
+// on tensor cores, transposed so that a block's result tiles are the next
+// product's a operand.  The serial part is 16 rows in place of 64; a column of
+// 64 rows a thread took 2.2 times as long (70 us for 2048 chunks of 128).
 template <bool F32, int DP>
 struct PrepSmem {
-    static constexpr int kTile = kChunk * DP * 2;
-    static constexpr int kPlanes = Planes<F32>::kInput;
-    static constexpr int kPitch = kChunk + 4;           // floats of a row of N
-    static constexpr int kK = 0, kQ = kPlanes * kTile, kN = 2 * kPlanes * kTile;
-    static constexpr int kBytes = kN + kChunk * kPitch * 4;
+    static constexpr int kTile = kChunk * DP * 2, kTri = kChunk * kChunk * 2;
+    static constexpr int NI = Planes<F32>::kInput, NP = Planes<F32>::kSplit;
+    // K and Q, later P, later L; N; the diagonal blocks of N in float32
+    static constexpr int kQ = NI * kTile;
+    static constexpr int kKQ = 2 * kQ > NP * kTri ? 2 * kQ : NP * kTri;
+    static constexpr int kN = kKQ, kDiag = kN + NP * kTri, kPitch = 17;
+    static constexpr int kBytes = kDiag + 4 * 16 * kPitch * 4;
 };
 
-// A block of four warps forms one chunk of one value head.
 template <bool F32, int DP>
 __global__ void __launch_bounds__(128)
 delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     using Sm = PrepSmem<F32, DP>;
+    constexpr int CH = DP / 8, NI = Sm::NI, NP = Sm::NP, kTri = Sm::kTri;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float g_hi[kChunk], g_lo[kChunk], s_beta[kChunk];
 
@@ -39,11 +49,12 @@ delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     const int b = head / in.Hv, h = head % in.Hv, ratio = in.Hv / in.Hk, hk = h / ratio;
     const int len = seq_len(in.lengths, b, in.T);
     const int t0 = chunk * kChunk;
-    if (t0 >= len) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (blockIdx.x == 0 && tid < 2) ws.status[tid] = 0;
+    if (t0 >= len) return;
     const uint32_t base = smem_u32(smem);
-    const uint32_t sK = base + Sm::kK, sQ = base + Sm::kQ;
-    float* sN = reinterpret_cast<float*>(smem + Sm::kN);
+    const uint32_t sK = base, sQ = base + Sm::kQ, sN = base + Sm::kN;
+    float* diag = reinterpret_cast<float*>(smem + Sm::kDiag);
 
     load_rows<F32, DP>(sK, in.k, row3(in.k_stride).at(b, hk, 0), in.k_stride[2], t0, len, in.D,
                        tid, 128);
@@ -51,51 +62,15 @@ delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
                        tid, 128);
     cp_commit();
 
-    // Running sums of log_alpha in double, kept as two floats: differences of
-    // sums far from 0 keep the accuracy of their own size.
-    float* gates = ws.gates(head, chunk);
-    if (warp == 0) {
-        const size_t at = ((size_t)b * in.Hv + h) * in.T + t0;
-        double s[2];
-        float bt[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = 2 * lane + i;
-            const bool on = t0 + t < len;
-            const float g = on ? in.log_alpha[at + t] : 0.f;
-            s[i] = g < kLogAlphaMin ? kLogAlphaMin : g;         // keeps NaN
-            bt[i] = on ? in.beta[at + t] : 0.f;
-        }
-        s[1] += s[0];
-        double run = s[1];
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const double y = __shfl_up_sync(~0u, run, d);
-            if (lane >= d) run += y;
-        }
-        const double before = run - s[1];
-        s[0] += before;
-        s[1] = run;
-        const double last = __shfl_sync(~0u, run, 31);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = 2 * lane + i;
-            g_hi[t] = (float)s[i];
-            g_lo[t] = (float)(s[i] - (double)g_hi[t]);
-            s_beta[t] = bt[i];
-            gates[t] = expf((float)s[i]);
-            gates[kChunk + t] = expf((float)(last - s[i]));
-            gates[2 * kChunk + t] = bt[i];
-            gates[3 * kChunk + t] = g_hi[t];
-            gates[4 * kChunk + t] = g_lo[t];
-        }
-    }
+    if (warp == 0)
+        chunk_gates(in, ((size_t)b * in.Hv + h) * in.T + t0, len - t0, ws.gates(head, chunk), g_hi,
+                    g_lo, s_beta, nullptr, lane);
     cp_wait<0>();
     __syncthreads();
 
     if (F32 && h % ratio == 0) {      // the planes of k and q that the chains load
         unsigned char* out = ws.planes(b * in.Hk + hk, chunk);
-        for (int i = tid; i < 2 * Sm::kPlanes * Sm::kTile / 16; i += 128)
+        for (int i = tid; i < 2 * Sm::kQ / 16; i += 128)
             reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(smem)[i];
     }
 
@@ -106,7 +81,6 @@ delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
         kk[i].zero();
         qk[i].zero();
     }
-    constexpr int CH = DP / 8, NI = Sm::kPlanes, NP = Planes<F32>::kSplit;
 #pragma unroll 1
     for (int ks = 0; ks < DP / 16; ++ks) {
         uint32_t ak[NI][4], aq[NI][4];
@@ -126,10 +100,9 @@ delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
             product_planes<NI, NI, NI>(qk + 2 * np, aq, bk);
         }
     }
+    __syncthreads();                  // K and Q have been read
     const int g = lane >> 2, tq = lane & 3;
     const float k2 = in.k_scale * in.k_scale, qk_scale = in.k_scale * in.q_scale;
-    __nv_bfloat16* pOut = ws.P(head, chunk);
-    __nv_bfloat16* lOut = ws.L(head, chunk);
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
         if (nt >= 2 * (warp + 1)) break;
@@ -143,43 +116,133 @@ delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
                 const float E = expf((g_hi[i] - g_hi[j + e]) + (g_lo[i] - g_lo[j + e]));
                 n[e] = i > j + e ? k2 * E * kk[nt][2 * r + e] : 0.f;
                 p[e] = i >= j + e ? qk_scale * E * qk[nt][2 * r + e] : 0.f;
+                if ((nt >> 1) == warp)
+                    diag[(warp * 16 + (i & 15)) * Sm::kPitch + ((j + e) & 15)] = n[e];
             }
-            *reinterpret_cast<float2*>(sN + i * Sm::kPitch + j) = make_float2(n[0], n[1]);
-            uint32_t w[NP];
-            split_bf16<NP>(p[0], p[1], w);
+            uint32_t wn[NP], wp[NP];
+            split_bf16<NP>(n[0], n[1], wn);
+            split_bf16<NP>(p[0], p[1], wp);
+            const uint32_t at = tile_at<8>(i, j >> 3) + (j & 7) * 2;
 #pragma unroll
-            for (int e = 0; e < NP; ++e)
-                *reinterpret_cast<uint32_t*>(pOut + (e * kChunk + i) * kChunk + j) = w[e];
+            for (int e = 0; e < NP; ++e) {
+                *reinterpret_cast<uint32_t*>(smem + e * kTri + at) = wp[e];
+                *reinterpret_cast<uint32_t*>(smem + Sm::kN + e * kTri + at) = wn[e];
+            }
         }
     }
     __syncthreads();
-
-    // L = N - N B L by forward substitution, a column a thread.  Rows up to the
-    // end of a row's 16-block are in sN; what lies above the diagonal is 0.
-    if (tid < kChunk) {
-        float x[kChunk];              // beta_j L_j,tid
+    {
+        unsigned char* out = reinterpret_cast<unsigned char*>(ws.P(head, chunk));
+        for (int i = tid; i < NP * kTri / 16; i += 128)
+            reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(smem)[i];
+    }
+    // the diagonal block of warp's rows: column `lane`
+    float l[16];
+    {
+        const float* n = diag + warp * 16 * Sm::kPitch;
+        const int c = lane & 15;
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) {
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < 16; ++i) {
+            float s = 0.f;
 #pragma unroll
-            for (int j = 0; j < i; j += 4) {
-                const float4 nr = *reinterpret_cast<const float4*>(sN + i * Sm::kPitch + j);
-                const float nv[4] = {nr.x, nr.y, nr.z, nr.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (j + e < i) s[e] += nv[e] * x[j + e];
-            }
-            float l = 0.f;
-            if (i > tid) l = sN[i * Sm::kPitch + tid] - ((s[0] + s[1]) + (s[2] + s[3]));
-            x[i] = s_beta[i] * l;
-#pragma unroll
-            for (int e = 0; e < NP; ++e) {
-                const __nv_bfloat16 w = __float2bfloat16_rn(l);
-                lOut[(e * kChunk + i) * kChunk + tid] = w;
-                l -= __bfloat162float(w);
-            }
+            for (int j = 0; j < i; ++j) s += n[i * Sm::kPitch + j] * (s_beta[warp * 16 + j] * l[j]);
+            l[i] = i > c ? n[i * Sm::kPitch + c] - s : 0.f;
         }
     }
+    __syncthreads();                  // P has left
+    if (lane < 16)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float x = l[i];
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                const __nv_bfloat16 w = __float2bfloat16_rn(x);
+                *reinterpret_cast<__nv_bfloat16*>(
+                    smem + e * kTri + tile_at<8>(warp * 16 + i, 2 * warp + (lane >> 3)) +
+                    (lane & 7) * 2) = w;
+                x -= __bfloat162float(w);
+            }
+        }
+    __syncthreads();
+
+    uint32_t bl[3][NP][4];            // (B L_jc)^T of the blocks so far
+    {
+        uint32_t w[NP][4];
+#pragma unroll
+        for (int e = 0; e < NP; ++e)
+            ldsm4_t(w[e], at_cols<8>(base + e * kTri, warp * 16, 2 * warp, lane));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = warp * 16 + 2 * tq + (i >> 1) * 8;
+            float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+            for (int e = NP - 1; e >= 0; --e) {
+                x0 += __uint_as_float(w[e][i] << 16);
+                x1 += __uint_as_float(w[e][i] & 0xffff0000u);
+            }
+            uint32_t p[NP];
+            split_bf16<NP>(s_beta[t] * x0, s_beta[t + 1] * x1, p);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) bl[0][e][i] = p[e];
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 4; ++d) {     // block row r = c + d
+        const int r = warp + d;
+        if (r > 3) break;
+        Acc C[2];
+        C[0].zero();
+        C[1].zero();
+#pragma unroll
+        for (int j = 0; j < d; ++j)
+            product_cols<NP, NP, NP, 8>(C, bl[j], sN, kTri, r * 16, 2 * (warp + j), lane);
+        float R[2][4] = {}, X[2][4];
+#pragma unroll
+        for (int e = NP - 1; e >= 0; --e) {       // N_rc transposed
+            uint32_t w[4];
+            ldsm4_t(w, at_rows<8>(sN + e * kTri, r * 16, 2 * warp, lane));
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    R[j][2 * i] += __uint_as_float(w[2 * i + j] << 16);
+                    R[j][2 * i + 1] += __uint_as_float(w[2 * i + j] & 0xffff0000u);
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                R[j][e] -= C[j][e];
+                X[j][e] = s_beta[r * 16 + j * 8 + 2 * tq + (e & 1)] * R[j][e];
+            }
+        uint32_t x[NP][4];
+        split_tiles<NP>(X[0], X[1], x);
+        C[0].zero();
+        C[1].zero();
+        product_cols<NP, NP, NP, 8>(C, x, base, kTri, r * 16, 2 * r, lane);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t w[2][NP];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                R[j][e] -= C[j][e];
+                X[j][e] = s_beta[r * 16 + j * 8 + 2 * tq + (e & 1)] * R[j][e];
+            }
+            split_bf16<NP>(R[j][0], R[j][1], w[0]);
+            split_bf16<NP>(R[j][2], R[j][3], w[1]);
+#pragma unroll
+            for (int e = 0; e < NP; ++e)
+                stsm2_t(base + e * kTri + tile_at<8>(r * 16 + j * 8 + (lane & 7),
+                                                     2 * warp + ((lane >> 3) & 1)),
+                        w[0][e], w[1][e]);
+        }
+        if (d < 3) split_tiles<NP>(X[0], X[1], bl[d]);
+    }
+    __syncthreads();
+    unsigned char* out = reinterpret_cast<unsigned char*>(ws.L(head, chunk));
+    for (int i = tid; i < NP * kTri / 16; i += 128)
+        reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(smem)[i];
 }
 
 // ---------------------------------------------------------------------------
@@ -273,8 +336,8 @@ delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) 
         }
         load_values<F32, SL>(st + Sm::oV, in.v, row3(in.v_stride).at(b, h, 0), in.v_stride[2], vb,
                              t0, len, D, tid, THREADS);
-        load_triangle<NP>(st + Sm::oL, ws.L(head, c), tid, THREADS);
-        if constexpr (!STATES) load_triangle<NP>(st + Sm::oP, ws.P(head, c), tid, THREADS);
+        copy_bytes(st + Sm::oL, ws.L(head, c), NP * Sm::kLP, tid, THREADS);
+        if constexpr (!STATES) copy_bytes(st + Sm::oP, ws.P(head, c), NP * Sm::kLP, tid, THREADS);
         copy_bytes(st + Sm::oGates, ws.gates(head, c), Sm::kGates, tid, THREADS);
         cp_commit();
     };
@@ -498,9 +561,10 @@ cudaError_t chain(const la_delta& in, const DeltaWs& ws, void* o, Row3 os, float
 template <bool F32, int DP>
 cudaError_t forward(const la_delta& in, const DeltaWs& ws, void* o, Row3 os, float* state_out,
                     cudaStream_t st) {
-    cudaError_t e = prep<F32, DP>(in, ws, st);
+    cudaError_t e = F32 ? prep<true, DP>(in, ws, st) : launch_delta_tc_prep(in, ws, false, st);
     if (e != cudaSuccess) return e;
-    return chain<F32, DP, 4, 1, false>(in, ws, o, os, state_out, st);
+    if constexpr (F32) return chain<F32, DP, 4, 1, false>(in, ws, o, os, state_out, st);
+    else return launch_delta_tc_chain(in, ws, o, os, state_out, false, st);
 }
 
 template <bool F32, int DP>

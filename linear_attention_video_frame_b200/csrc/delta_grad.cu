@@ -89,8 +89,8 @@ delta_reverse_kernel(la_delta in, DeltaGrad grad, DeltaWs ws) {
         }
         load_values<F32, SL>(st + Sm::oV, grad.d_o, row3(grad.do_stride).at(b, h, 0),
                              grad.do_stride[2], vb, t0, len, D, tid, THREADS);
-        load_triangle<NP>(st + Sm::oL, ws.L(head, c), tid, THREADS);
-        load_triangle<NP>(st + Sm::oP, ws.P(head, c), tid, THREADS);
+        copy_bytes(st + Sm::oL, ws.L(head, c), NP * Sm::kLP, tid, THREADS);
+        copy_bytes(st + Sm::oP, ws.P(head, c), NP * Sm::kLP, tid, THREADS);
         copy_bytes(st + Sm::oGates, ws.gates(head, c), Sm::kGates, tid, THREADS);
         cp_commit();
     };

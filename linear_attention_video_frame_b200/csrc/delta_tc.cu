@@ -1,0 +1,447 @@
+// The forward chain of the chunked gated delta rule on tcgen05 (bf16 inputs);
+// Kt, Pt and the mathematics are in delta_tc_prep.cu, the operands' layout in
+// delta_tc.cuh.
+//
+// One block walks the chunks of one head.  The chain itself is
+//   MMA warp   KS = S^T K^T   ->   compute warps   X = B (V - gamma o KS)
+//   MMA warp   X Kt           ->   compute warps   S = gamma_63 S + X Kt
+// with an mbarrier each way; beside it run QS and X Pt^T with the outputs, or
+// X L^T with Z = Y - X L^T for the backward pass.  Each of the 16 compute warps
+// owns 32 value columns (its quarter of the lanes) and a quarter of the tokens
+// (16) and of the key rows.  Three load warps keep the next chunk in flight.
+#include "delta_tc.cuh"
+
+namespace la {
+namespace {
+using namespace dtc;
+
+// Shared memory: two stages of K, Q, V and the gates; one of Kt and Pt (or L),
+// which are needed for a part of a chunk's time only.
+template <int DP, bool STATES>
+struct ChainTc {
+    static constexpr int kHalf = STATES ? 8192 : 16384;     // K (and Q) rows of 64 columns
+    static constexpr int oKQ = 0, oV = (DP / 64) * kHalf, oGates = oV + kChunk * DP * 2,
+                         kStage = oGates + 1024;
+    static constexpr int kKt = (DP / 64) * 3 * 8192, kPt = (STATES ? 3 : 2) * kTri;
+    static constexpr int oKt = 2 * kStage, oPt = oKt + kKt, oOut = oPt + kPt;
+    // a warp's rows on their way out (a plane of 32 x 32 of the state, or 16 tokens x 32)
+    static constexpr int kOut = STATES ? 2048 : 1024;
+    static constexpr int kBytes = oOut + kComputeWarps * kOut + 1024;
+};
+// Tensor-memory columns: the first planes of S, later X Kt | the last plane of
+// S | KS | QS | X Pt^T or X L^T | the planes of X.
+constexpr uint32_t cUpd = 0, cLo = 128, cKS = 192, cQS = 256, cPX = 320, cX = 384;
+
+struct ChainArgs {
+    la_delta in;
+    DeltaWs ws;
+    void* o;
+    Row3 os;
+    float* state_out;
+};
+
+template <int DP, bool STATES>
+__global__ void __launch_bounds__(kThreads, 1)
+delta_tc_chain_kernel(ChainArgs args) {
+    using Sm = ChainTc<DP, STATES>;
+    constexpr int NK = DP / 4;                  // key rows of a thread
+    // The update and the next KS go by halves of the key rows, so that half of
+    // the warps work on their part of S while the other half's is multiplied.
+    constexpr int kHalves = DP / 64;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = tc::align1024(smem_raw);
+    __shared__ uint64_t full[2], empty[2], full_kt, full_pt, ready_s[2], ready_x;
+    __shared__ uint64_t done_ks, done_qs, done_upd[2], done_px, done_all;
+    __shared__ uint32_t s_tmem, s_abort;
+
+    const la_delta& in = args.in;
+    const DeltaWs& ws = args.ws;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);
+    const int head = blockIdx.x, b = head / in.Hv, h = head % in.Hv, hk = h / (in.Hv / in.Hk);
+    const int D = in.D;
+    const int len = seq_len(in.lengths, b, in.T);
+    const int c0 = 0, c1 = (len + kChunk - 1) / kChunk, n = c1 - c0;
+    const tc::Abort ab{&s_abort, ws.status};
+
+    if (tid == 0) {
+        s_abort = 0;
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&full[i], kRowThreads);
+            tc::mbar_init(&empty[i], kComputeWarps);
+            tc::mbar_init(&ready_s[i], kComputeWarps / kHalves);
+            tc::mbar_init(&done_upd[i], 1);
+        }
+        for (uint64_t* bar : {&full_kt, &full_pt, &done_ks, &done_qs, &done_px, &done_all})
+            tc::mbar_init(bar, 1);
+        tc::mbar_init(&ready_x, kComputeWarps);
+        tc::fence_mbar_init();
+    }
+    if (warp == 0) {
+        tc::tmem_alloc(&s_tmem, 512);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tm = s_tmem;
+
+    if (warp >= kFirstCompute) {
+        // ---------------------------------------------------------------- compute
+        // 16 warps x 104 + 4 x 64 = the launch's 20 x 96 registers a thread
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        const int quarter = warp & 3, part = (warp - kFirstCompute) >> 2;
+        const bool alive = quarter * 32 < D;        // else the warp only keeps step
+        const int g = lane >> 2, tq = lane & 3;
+        const int v0 = quarter * 32;                // value columns v0 + 16 h + 8 r + g
+        const int k0 = part * NK, tok = part * 16, side = k0 / 64;
+        const uint32_t at = tc::tmem_addr(tm, quarter * 32, 0);
+        const uint32_t aS[3] = {at + k0, at + k0 + NK / 2, at + cLo + k0 / 2};
+        const uint32_t aX[3] = {at + cX + part * 8, at + cX + 32 + part * 8, at + cX + 64 + part * 8};
+        unsigned char* buf = smem + Sm::oOut + (warp - kFirstCompute) * Sm::kOut;
+        const uint32_t buf_a = smem_u32(buf);
+
+        Frag S[NK / 16];                            // key rows k0 + 16 i + 8 j + 2 tq + (e & 1)
+        auto each_state = [&](auto&& f) {
+#pragma unroll
+            for (int i = 0; i < NK / 16; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int k = k0 + 16 * i + 8 * j + 2 * tq + (e & 1);
+                            const int v = v0 + 16 * h + 8 * (e >> 1) + g;
+                            f(S[i][h][j][e], ((size_t)head * D + k) * D + v, k < D && v < D);
+                        }
+        };
+        each_state([&](float& x, size_t p, bool on) {
+            x = in.state_in && on ? in.state_in[p] : 0.f;
+        });
+        // The state as operand planes: [64 key rows][plane][value column][128 bytes],
+        // swizzled, by way of shared memory.
+        auto put_state = [&](int c) {
+            unsigned char* out = reinterpret_cast<unsigned char*>(ws.states(head, c));
+            uint32_t w[3][NK / 16][2][2][2];
+#pragma unroll
+            for (int i = 0; i < NK / 16; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            uint32_t p[3];
+                            cut_planes(S[i][h][j][2 * r], S[i][h][j][2 * r + 1], p);
+#pragma unroll
+                            for (int e = 0; e < 3; ++e) w[e][i][h][r][j] = p[e];
+                        }
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+                // rows of NK key rows (2 NK bytes), 8 value columns a matrix
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int row = 16 * h + 8 * r + (lane & 7);
+                        if constexpr (NK == 32)
+                            stsm4(buf_a + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4),
+                                  w[e][0][h][r][0], w[e][0][h][r][1], w[e][1][h][r][0],
+                                  w[e][1][h][r][1]);
+                        else if (r == 0)
+                            stsm4(buf_a + (16 * h + (lane & 7) + 8 * ((lane >> 3) & 1)) * 32 +
+                                      ((lane >> 4) << 4),
+                                  w[e][0][h][0][0], w[e][0][h][1][0], w[e][0][h][0][1],
+                                  w[e][0][h][1][1]);
+                    }
+                __syncwarp();
+#pragma unroll
+                for (int i = lane; i < 32 * (NK / 8); i += 32) {
+                    const int row = i / (NK / 8), p = i % (NK / 8), v = v0 + row;
+                    const int key = k0 + 8 * p;
+                    if (v < D && key < D)
+                        *reinterpret_cast<uint4*>(out + ((size_t)((key >> 6) * 3 + e) * D + v) * 128 +
+                                                  ((((key >> 3) & 7) ^ (v & 7)) << 4)) =
+                            *reinterpret_cast<const uint4*>(
+                                buf + (NK == 32 ? row * 64 + ((p ^ ((row >> 1) & 3)) << 4)
+                                                : row * 32 + (p << 4)));
+                }
+            }
+        };
+        if (n > 0) {
+            if (alive)
+#pragma unroll
+                for (int j = 0; j < NK / 16; ++j) store_a(aS, 8 * j, S[j]);
+            arrive(&ready_s[side], lane);
+        }
+        if constexpr (STATES)
+            if (alive) put_state(c0);
+
+        // The outputs of a chunk, 16 tokens x 32 columns a warp.  They leave one chunk
+        // late, while the tensor core has the chain.
+        uint32_t ow[2][2][2];
+        auto put_out = [&](int c) {
+            __syncwarp();
+            stage_rows(buf_a, ow, lane);
+            __syncwarp();
+            const int col = v0 + (lane & 3) * 8, t0 = c * kChunk + tok + (lane >> 2);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (col < D && t0 + 8 * i < len)
+                    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(args.o) +
+                                              args.os.at(b, h, t0 + 8 * i) + col) =
+                        staged_row(buf, i, lane);
+        };
+        auto each = [&](auto&& f) {                 // of a fragment: f(h, j, e)
+#pragma unroll
+            for (int h_ = 0; h_ < 2; ++h_)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f(h_, j, e);
+        };
+
+        for (int i = 0; i < n; ++i) {
+            const int c = c0 + i, st = i & 1, ph = i & 1;
+            const unsigned char* stage = smem + st * Sm::kStage;
+            const float* gates = reinterpret_cast<const float*>(stage + Sm::oGates);
+            Frag x, y;
+            Factors ga, be, f;
+            tc::mbar_wait(&full[st], (i >> 1) & 1, ab, 1);
+            factors(ga, gates + tok, tq);
+            factors(be, gates + 2 * kChunk + tok, tq);
+            if (alive) load_rows_frag(y, smem_u32(stage) + Sm::oV, 8192, tok, v0, lane);
+            const float gc = gates[kChunk - 1];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) f[j] = make_float2(-in.k_scale * ga[j].x, -in.k_scale * ga[j].y);
+            tc::mbar_wait(&done_ks, ph, ab, 2);
+            tc::tc_fence_after();
+            if (alive) {
+                load_frag(x, at + cKS + tok);
+                tc::tmem_wait_ld();
+                each([&](int a, int j, int e) {
+                    y[a][j][e] += factor(f, j, e) * x[a][j][e];
+                    x[a][j][e] = factor(be, j, e) * y[a][j][e];
+                });
+                store_a(aX, 0, x);
+            }
+            arrive(&ready_x, lane);
+            if constexpr (!STATES) {
+                if (alive && i > 0) put_out(c - 1);
+                tc::mbar_wait(&done_qs, ph, ab, 5);
+                tc::tc_fence_after();
+                if (alive) {
+                    load_frag(y, at + cQS + tok);
+                    tc::tmem_wait_ld();
+                    each([&](int a, int j, int e) {
+                        y[a][j][e] *= in.q_scale * factor(ga, j, e);
+                    });
+                }
+            }
+
+            tc::mbar_wait(&done_upd[side], ph, ab, 3);
+            tc::tc_fence_after();
+            if (alive) {
+#pragma unroll
+                for (int j = 0; j < NK / 16; ++j) {
+                    load_frag(x, at + cUpd + k0 + 16 * j);
+                    tc::tmem_wait_ld();
+                    each([&](int a, int t, int e) {
+                        S[j][a][t][e] = gc * S[j][a][t][e] + x[a][t][e];
+                    });
+                    // the planes go over this part's products, of which the second half
+                    // is read after them: they are held back
+                    if (NK == 16 && i + 1 < n) store_a(aS, 0, S[j]);
+                }
+                if (NK > 16 && i + 1 < n)
+#pragma unroll
+                    for (int j = 0; j < NK / 16; ++j) store_a(aS, 8 * j, S[j]);
+            }
+            if (i + 1 < n) arrive(&ready_s[side], lane);
+
+            if constexpr (STATES) {
+                if (alive) put_state(c + 1);
+                tc::mbar_wait(&done_px, ph, ab, 4);
+                tc::tc_fence_after();
+                if (alive) {
+                    // Z as operand planes: [64 value columns][plane][token][128 bytes], swizzled
+                    load_frag(x, at + cPX + tok);
+                    tc::tmem_wait_ld();
+                    uint32_t w[3][2][2][2];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int a = k >> 2, j = (k >> 1) & 1, r = k & 1;
+                        uint32_t p[3];
+                        cut_planes(y[a][j][2 * r] - x[a][j][2 * r],
+                                   y[a][j][2 * r + 1] - x[a][j][2 * r + 1], p);
+#pragma unroll
+                        for (int e = 0; e < 3; ++e) w[e][a][j][r] = p[e];
+                    }
+                    unsigned char* out = reinterpret_cast<unsigned char*>(ws.Z(head, c));
+                    const int col = v0 + (lane & 3) * 8;
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) {
+                        __syncwarp();
+                        stage_rows(buf_a, w[e], lane);
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int t = tok + (lane >> 2) + 8 * k;
+                            if (col < D)
+                                *reinterpret_cast<uint4*>(
+                                    out + ((col >> 6) * 3 + e) * 8192 + t * 128 +
+                                    ((((col >> 3) & 7) ^ (t & 7)) << 4)) = staged_row(buf, k, lane);
+                        }
+                    }
+                }
+            } else {
+                tc::mbar_wait(&done_px, ph, ab, 6);
+                tc::tc_fence_after();
+                if (alive) {
+                    load_frag(x, at + cPX + tok);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int a = k >> 2, j = (k >> 1) & 1, r = k & 1;
+                        ow[a][j][r] = pack_bf16(y[a][j][2 * r] + x[a][j][2 * r],
+                                                y[a][j][2 * r + 1] + x[a][j][2 * r + 1]);
+                    }
+                }
+            }
+            // done_px was waited for, so the stage's last products are done as well
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&empty[st]);
+        }
+        if constexpr (!STATES)
+            if (alive && n > 0) put_out(c1 - 1);
+        if (args.state_out)
+            each_state([&](float& x, size_t p, bool on) {
+                if (on) args.state_out[p] = x;
+            });
+    } else if (warp > 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        // ------------------------------------------------------------------ load
+        const int job = warp - 1;                       // K | V and the gates | Kt, Pt or L
+        if (job < 2) {
+            const Row3 rows3 = row3(job ? in.v_stride : in.k_stride), q3 = row3(in.q_stride);
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(job ? in.v : in.k) +
+                                       rows3.at(b, job ? h : hk, 0);
+            // and half of Q's rows each
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(in.q) + q3.at(b, hk, 32 * job);
+            for (int i = 0; i < n; ++i) {
+                const int c = c0 + i, st = i & 1, t0 = c * kChunk, rows = len - t0;
+                if (i >= 2) tc::mbar_wait(&empty[st], ((i >> 1) - 1) & 1, ab, 7);
+                const uint32_t sa = smem_u32(smem + st * Sm::kStage);
+                if (job == 0) {
+                    load_tile(sa + Sm::oKQ, Sm::kHalf, src + t0 * rows3.t, rows3.t, rows, D,
+                                        lane);
+                } else {
+                    load_tile(sa + Sm::oV, 8192, src + t0 * rows3.t, rows3.t, rows, D, lane);
+                    for (int k = lane; k < 3 * kChunk / 4; k += 32)
+                        cp16(sa + Sm::oGates + k * 16, ws.gates(head, c) + k * 4, true);
+                }
+                if constexpr (!STATES)
+                    if (rows > 32 * job)
+                        load_tile<32>(sa + Sm::oKQ + 8192 + 4096 * job, Sm::kHalf,
+                                                q + t0 * q3.t, q3.t, rows - 32 * job, D, lane);
+                cp_commit();
+                if (i + 1 < n)                          // the next chunk's, towards the L2
+                    prefetch_lines(job == 0 ? ws.Kt(head, c + 1)
+                                            : reinterpret_cast<const unsigned char*>(
+                                                  STATES ? ws.L(head, c + 1) : ws.P(head, c + 1)),
+                                   job == 0 ? Sm::kKt : Sm::kPt, lane);
+                cp_wait<0>();
+                tc::fence_proxy_async_smem();
+                tc::mbar_arrive(&full[st]);
+            }
+        } else if (lane == 0) {
+            for (int i = 0; i < n; ++i) {
+                if (i >= 1) tc::mbar_wait(&done_upd[kHalves - 1], (i - 1) & 1, ab, 8);
+                tc::mbar_expect_tx(&full_kt, Sm::kKt);
+                tc::bulk_load(smem + Sm::oKt, ws.Kt(head, c0 + i), Sm::kKt, &full_kt);
+                if (i >= 1) tc::mbar_wait(&done_px, (i - 1) & 1, ab, 9);
+                tc::mbar_expect_tx(&full_pt, Sm::kPt);
+                tc::bulk_load(smem + Sm::oPt, STATES ? ws.L(head, c0 + i) : ws.P(head, c0 + i),
+                              Sm::kPt, &full_pt);
+            }
+            if (n > 0 && tc::aborted(ab)) {
+                tc::mbar_drain(&full_kt, (n - 1) & 1);
+                tc::mbar_drain(&full_pt, (n - 1) & 1);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        // ------------------------------------------------------------------- MMA
+        const uint32_t base = __shfl_sync(~0u, smem_u32(smem), 0);
+        const uint32_t tm = __shfl_sync(~0u, s_tmem, 0);
+        if (tc::elect_one()) {
+            for (int i = 0; i < n; ++i) {
+                const int st = i & 1, ph = i & 1;
+                const uint32_t stage = base + st * Sm::kStage;
+                tc::mbar_wait(&full[st], (i >> 1) & 1, ab, 10);
+                tc::mbar_wait(&ready_s[0], ph, ab, 11);
+                if (ab.raised()) break;
+                tc::tc_fence_after();
+                mma_state<3, DP, 0, 4>(tm + cKS, tm, cLo, stage + Sm::oKQ, Sm::kHalf, D / 16);
+                if constexpr (kHalves > 1) {
+                    tc::mbar_wait(&ready_s[1], ph, ab, 17);
+                    if (ab.raised()) break;
+                    tc::tc_fence_after();
+                    mma_state<3, DP, 4, 8>(tm + cKS, tm, cLo, stage + Sm::oKQ, Sm::kHalf, D / 16);
+                }
+                tc::mma_commit(&done_ks);
+                if constexpr (!STATES) {
+                    mma_state<2, DP, 0, DP / 16>(tm + cQS, tm, cLo, stage + Sm::oKQ + 8192, Sm::kHalf,
+                                     D / 16);
+                    tc::mma_commit(&done_qs);
+                }
+                tc::mbar_wait(&full_kt, ph, ab, 12);
+                if constexpr (!STATES) tc::mbar_wait(&done_qs, ph, ab, 16);  // it reads S
+                tc::mbar_wait(&ready_x, ph, ab, 13);
+                if (ab.raised()) break;
+                tc::tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < kHalves; ++j) {
+                    mma_update<3>(tm + cUpd + 64 * j, tm + cX, base + Sm::oKt + j * 3 * 8192, 0, 8192,
+                                  D - 64 * j < 64 ? D - 64 * j : 64);
+                    tc::mma_commit(&done_upd[j]);
+                }
+                tc::mbar_wait(&full_pt, ph, ab, 14);
+                if (ab.raised()) break;
+                mma_lower<STATES ? 3 : 2>(tm + cPX, tm + cX, base + Sm::oPt);
+                tc::mma_commit(&done_px);
+            }
+            tc::mma_commit(&done_all);
+            tc::mbar_drain(&done_all, 0);       // nothing in flight when the memory is freed
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tm, 512);
+    }
+}
+
+template <int DP, bool STATES>
+cudaError_t chain(const ChainArgs& a, cudaStream_t st) {
+    auto* kernel = delta_tc_chain_kernel<DP, STATES>;
+    constexpr int bytes = ChainTc<DP, STATES>::kBytes;
+    static_assert(bytes <= 227 * 1024, "shared memory of a block");
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<a.in.B * a.in.Hv, kThreads, bytes, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_delta_tc_chain(const la_delta& in, const DeltaWs& ws, void* o, Row3 os,
+                                  float* state_out, bool states, cudaStream_t st) {
+    const ChainArgs a{in, ws, o, os, state_out};
+    if (states) return in.D <= 64 ? chain<64, true>(a, st) : chain<128, true>(a, st);
+    return in.D <= 64 ? chain<64, false>(a, st) : chain<128, false>(a, st);
+}
+
+}  // namespace la

@@ -19,11 +19,13 @@ template <bool F32> struct Planes {
 constexpr int kGateRows = 5;
 
 // What the kernels of a call hand to one another.  L and P are [64][64] bf16
-// planes; blocks of 16 above the diagonal are not written.  States are images
+// planes as shared-memory tiles (tile_at<8>, which is also the tensor core's
+// 128-byte swizzle); blocks of 16 above the diagonal hold anything.  States are images
 // [value column][key row] of DP columns in planes; Z and dX are rows
 // [token][value column] of DP columns in planes.
 struct DeltaWs {
-    unsigned char *gates_, *L_, *P_, *planes_, *states_, *dstates_, *Z_, *dX_;
+    unsigned int* status;        // header of the workspace (la_query_device_status)
+    unsigned char *gates_, *L_, *P_, *Kt_, *planes_, *states_, *dstates_, *Z_, *dX_;
     int chunks;          // per head
     int DP, D, NP;
     size_t bytes;
@@ -37,6 +39,7 @@ struct DeltaWs {
         const size_t n = (size_t)B * Hv * w.chunks, nk = (size_t)B * Hk * w.chunks;
         size_t at = kWsHeaderBytes;
         unsigned char* p = static_cast<unsigned char*>(mem);
+        w.status = static_cast<unsigned int*>(mem);
         auto take = [&](size_t size) {
             unsigned char* r = p + at;
             at = align_up(at + size, 256);
@@ -45,6 +48,7 @@ struct DeltaWs {
         w.gates_ = take(n * kGateRows * kChunk * 4);
         w.L_ = take(n * w.NP * 2 * kChunk * kChunk);
         w.P_ = take(n * w.NP * 2 * kChunk * kChunk);
+        w.Kt_ = take(dt == LA_BF16 ? n * 3 * w.plane_bytes() : 0);
         w.planes_ = take(dt == LA_F32 ? nk * 2 * w.NP * w.plane_bytes() : 0);
         if (backward) {
             w.states_ = take((size_t)B * Hv * (w.chunks + 1) * w.image_bytes());
@@ -67,6 +71,10 @@ struct DeltaWs {
     __device__ __nv_bfloat16* P(int head, int c) const {
         return reinterpret_cast<__nv_bfloat16*>(P_) + at(head, c) * NP * kChunk * kChunk;
     }
+    // bf16 inputs: Kt as [half of 64 columns][plane][64 rows of 128 bytes], swizzled
+    __device__ unsigned char* Kt(int head, int c) const {
+        return Kt_ + at(head, c) * 3 * plane_bytes();
+    }
     // float32 inputs: the planes of K, then of Q, as shared-memory tiles
     __device__ unsigned char* planes(int khead, int c) const {
         return planes_ + ((size_t)khead * chunks + c) * 2 * NP * plane_bytes();
@@ -86,6 +94,13 @@ struct DeltaWs {
     }
 };
 
+// Kt, Pt (and L) of every chunk (delta_tc_prep.cu)
+cudaError_t launch_delta_tc_prep(const la_delta& in, const DeltaWs& ws, bool backward,
+                                 cudaStream_t st);
+// forward chain on tcgen05 (delta_tc.cu), with outputs or with states for the
+// backward pass
+cudaError_t launch_delta_tc_chain(const la_delta& in, const DeltaWs& ws, void* o, Row3 os,
+                                  float* state_out, bool states, cudaStream_t st);
 // prep and forward chain of the backward pass (delta_chunk.cu)
 cudaError_t launch_delta_states(const la_delta& in, const DeltaWs& ws, cudaStream_t st);
 
@@ -134,17 +149,6 @@ __device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, int by
         cp16(dst + i * 16, static_cast<const unsigned char*>(src) + i * 16, true);
 }
 
-// NP planes of a [64][64] lower triangle, whole 16-blocks up to the diagonal.
-template <int NP>
-__device__ __forceinline__ void load_triangle(uint32_t dst, const __nv_bfloat16* src, int tid,
-                                              int threads) {
-    for (int i = tid; i < NP * kChunk * 8; i += threads) {
-        const int r = (i >> 3) & 63, c = i & 7;
-        if (c < 2 * ((r >> 4) + 1))
-            cp16(dst + (i >> 9) * (kChunk * kChunk * 2) + tile_at<8>(r, c), src + i * 8, true);
-    }
-}
-
 // A product tile in two sums: the leading planes' product, and the products
 // with a lower plane.  The tensor core rounds its sums towards zero, so a sum
 // loses up to half a last place for each product added to it: few are added to
@@ -191,6 +195,48 @@ __device__ __forceinline__ void product_rows(Acc* c, const uint32_t (&a)[NA][4],
 #pragma unroll
     for (int j = 0; j < NB; ++j) ldsm4_t(b[j], at_rows<CH>(tile + j * plane, row, piece, lane));
     product_planes<NP, NA, NB>(c, a, b);
+}
+
+// The gates of a chunk's 64 tokens, by one warp.  Running sums of log_alpha in
+// double, kept as two floats: differences of sums far from 0 keep the accuracy
+// of their own size.  Tokens from `on` on have alpha = 1 and beta = 0.
+__device__ __forceinline__ void chunk_gates(const la_delta& in, size_t at, int on, float* gates,
+                                            float* g_hi, float* g_lo, float* beta, float* tail,
+                                            int lane) {
+    double s[2];
+    float bt[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        const float g = t < on ? in.log_alpha[at + t] : 0.f;
+        s[i] = g < kLogAlphaMin ? kLogAlphaMin : g;         // keeps NaN
+        bt[i] = t < on ? in.beta[at + t] : 0.f;
+    }
+    s[1] += s[0];
+    double run = s[1];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const double y = __shfl_up_sync(~0u, run, d);
+        if (lane >= d) run += y;
+    }
+    s[0] += run - s[1];
+    s[1] = run;
+    const double last = __shfl_sync(~0u, run, 31);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        const float hi = (float)s[i], lo = (float)(s[i] - (double)hi);
+        const float to_end = expf((float)(last - s[i]));
+        g_hi[t] = hi;
+        g_lo[t] = lo;
+        beta[t] = bt[i];
+        if (tail) tail[t] = to_end;
+        gates[t] = expf(hi);
+        gates[kChunk + t] = to_end;
+        gates[2 * kChunk + t] = bt[i];
+        gates[3 * kChunk + t] = hi;
+        gates[4 * kChunk + t] = lo;
+    }
 }
 
 __device__ __forceinline__ void group_sync(int id, int threads) {

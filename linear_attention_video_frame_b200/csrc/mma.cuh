@@ -45,6 +45,18 @@ __device__ __forceinline__ void stsm2_t(uint32_t addr, uint32_t r0, uint32_t r1)
                  :: "r"(addr), "r"(r0), "r"(r1) : "memory");
 }
 
+// Four 8 x 8 matrices; lane i gives the address of row i % 8 of matrix i / 8.
+__device__ __forceinline__ void stsm4(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2,
+                                      uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};"
+                 :: "r"(addr), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
+}
+__device__ __forceinline__ void stsm4_t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2,
+                                        uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
+                 :: "r"(addr), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
+}
+
 // Two floats as a bf16 pair (x0 in the low half).
 __device__ __forceinline__ uint32_t pack_bf16(float x0, float x1) {
     const __nv_bfloat162 t = __floats2bfloat162_rn(x0, x1);

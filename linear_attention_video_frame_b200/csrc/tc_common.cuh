@@ -260,6 +260,17 @@ __device__ __forceinline__ void tc_fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// True in one thread of a converged warp.  Code under it is known to run in one
+// thread, so the operands of its MMAs go to uniform registers directly; under
+// `lane == 0` each costs a loop over the threads that might be there (50 cycles
+// an MMA, 100 beside busy warps, in place of 23).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e = 0;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t@p mov.s32 %0, 1;\n\t}"
+                 : "+r"(e));
+    return e != 0;
+}
+
 // D[tmem] (+)= A[smem] * B[smem]^T  (kind::f16, bf16 inputs, f32 accumulate).
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                          uint32_t idesc, uint32_t accumulate) {
@@ -267,6 +278,16 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
         ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// The same with A in tensor memory: lane = row, each 32-bit column two bf16
+// values of consecutive K.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
 // Arrive once on `bar` when all previously issued MMAs of this thread complete.
@@ -366,6 +387,22 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
           "r"(__float_as_uint(v[11])), "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])),
           "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15]))
         : "memory");
+}
+// 16 lanes in the fragment layout of warp-level matrix products: of 8 (4 X)
+// columns, thread (g = lane / 4, t = lane % 4) holds
+//   256 bit: (lane g, columns 2t, 2t + 1), (lane g + 8, the same) for each 8 columns
+//   128 bit: (lane g, column t), (lane g + 8, column t)           for each 4 columns
+__device__ __forceinline__ void tmem_ld_frag2(uint32_t taddr, float (&v)[2][4]) {     // 16 columns
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7]) : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st_frag2(uint32_t taddr, const uint32_t (&v)[4]) {  // 8 columns
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};"
+                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
