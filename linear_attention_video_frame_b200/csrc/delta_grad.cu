@@ -718,8 +718,17 @@ cudaError_t backward(const la_delta& in, const DeltaGrad& g, const DeltaWs& ws, 
 cudaError_t launch_delta_backward(const la_delta& in, const DeltaGrad& g, void* ws_mem,
                                   cudaStream_t st) {
     const DeltaWs ws = DeltaWs::layout(ws_mem, 1, in.dt, in.B, in.Hk, in.Hv, in.T, in.D);
-    if (in.dt == LA_BF16)
-        return in.D <= 64 ? backward<false, 64>(in, g, ws, st) : backward<false, 128>(in, g, ws, st);
+    if (in.dt == LA_BF16) {
+        cudaError_t e = cudaSuccess;
+        if (in.T > 0) {
+            if ((e = launch_delta_tc_prep(in, ws, true, st)) != cudaSuccess) return e;
+            if ((e = launch_delta_tc_chain(in, ws, nullptr, Row3{0, 0, 0}, nullptr, true, st)) !=
+                cudaSuccess)
+                return e;
+        }
+        if ((e = launch_delta_tc_reverse(in, g, ws, st)) != cudaSuccess || in.T == 0) return e;
+        return launch_delta_tc_grad(in, g, ws, st);
+    }
     return in.D <= 64 ? backward<true, 64>(in, g, ws, st) : backward<true, 128>(in, g, ws, st);
 }
 

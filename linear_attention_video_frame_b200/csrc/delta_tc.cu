@@ -24,8 +24,7 @@ struct ChainTc {
                          kStage = oGates + 1024;
     static constexpr int kKt = (DP / 64) * 3 * 8192, kPt = (STATES ? 3 : 2) * kTri;
     static constexpr int oKt = 2 * kStage, oPt = oKt + kKt, oOut = oPt + kPt;
-    // a warp's rows on their way out (a plane of 32 x 32 of the state, or 16 tokens x 32)
-    static constexpr int kOut = STATES ? 2048 : 1024;
+    static constexpr int kOut = STATES ? 0 : 1024;      // a warp's outputs on their way
     static constexpr int kBytes = oOut + kComputeWarps * kOut + 1024;
 };
 // Tensor-memory columns: the first planes of S, later X Kt | the last plane of
@@ -98,7 +97,6 @@ delta_tc_chain_kernel(ChainArgs args) {
         const uint32_t aS[3] = {at + k0, at + k0 + NK / 2, at + cLo + k0 / 2};
         const uint32_t aX[3] = {at + cX + part * 8, at + cX + 32 + part * 8, at + cX + 64 + part * 8};
         unsigned char* buf = smem + Sm::oOut + (warp - kFirstCompute) * Sm::kOut;
-        const uint32_t buf_a = smem_u32(buf);
 
         Frag S[NK / 16];                            // key rows k0 + 16 i + 8 j + 2 tq + (e & 1)
         auto each_state = [&](auto&& f) {
@@ -118,56 +116,11 @@ delta_tc_chain_kernel(ChainArgs args) {
         each_state([&](float& x, size_t p, bool on) {
             x = in.state_in && on ? in.state_in[p] : 0.f;
         });
-        // The state as operand planes: [64 key rows][plane][value column][128 bytes],
-        // swizzled, by way of shared memory.
-        auto put_state = [&](int c) {
-            unsigned char* out = reinterpret_cast<unsigned char*>(ws.states(head, c));
-            uint32_t w[3][NK / 16][2][2][2];
+        const int cw = warp - kFirstCompute;
+        auto put_state = [&](int c) {               // for the backward pass
 #pragma unroll
             for (int i = 0; i < NK / 16; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            uint32_t p[3];
-                            cut_planes(S[i][h][j][2 * r], S[i][h][j][2 * r + 1], p);
-#pragma unroll
-                            for (int e = 0; e < 3; ++e) w[e][i][h][r][j] = p[e];
-                        }
-#pragma unroll
-            for (int e = 0; e < 3; ++e) {
-                // rows of NK key rows (2 NK bytes), 8 value columns a matrix
-                __syncwarp();
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int row = 16 * h + 8 * r + (lane & 7);
-                        if constexpr (NK == 32)
-                            stsm4(buf_a + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4),
-                                  w[e][0][h][r][0], w[e][0][h][r][1], w[e][1][h][r][0],
-                                  w[e][1][h][r][1]);
-                        else if (r == 0)
-                            stsm4(buf_a + (16 * h + (lane & 7) + 8 * ((lane >> 3) & 1)) * 32 +
-                                      ((lane >> 4) << 4),
-                                  w[e][0][h][0][0], w[e][0][h][1][0], w[e][0][h][0][1],
-                                  w[e][0][h][1][1]);
-                    }
-                __syncwarp();
-#pragma unroll
-                for (int i = lane; i < 32 * (NK / 8); i += 32) {
-                    const int row = i / (NK / 8), p = i % (NK / 8), v = v0 + row;
-                    const int key = k0 + 8 * p;
-                    if (v < D && key < D)
-                        *reinterpret_cast<uint4*>(out + ((size_t)((key >> 6) * 3 + e) * D + v) * 128 +
-                                                  ((((key >> 3) & 7) ^ (v & 7)) << 4)) =
-                            *reinterpret_cast<const uint4*>(
-                                buf + (NK == 32 ? row * 64 + ((p ^ ((row >> 1) & 3)) << 4)
-                                                : row * 32 + (p << 4)));
-                }
-            }
+                save_frag(ws.state_frags(head, c), NK / 4, i, S[i], cw, lane);
         };
         if (n > 0) {
             if (alive)
@@ -183,7 +136,7 @@ delta_tc_chain_kernel(ChainArgs args) {
         uint32_t ow[2][2][2];
         auto put_out = [&](int c) {
             __syncwarp();
-            stage_rows(buf_a, ow, lane);
+            stage_rows(smem_u32(buf), ow, lane);
             __syncwarp();
             const int col = v0 + (lane & 3) * 8, t0 = c * kChunk + tok + (lane >> 2);
 #pragma unroll
@@ -193,15 +146,6 @@ delta_tc_chain_kernel(ChainArgs args) {
                                               args.os.at(b, h, t0 + 8 * i) + col) =
                         staged_row(buf, i, lane);
         };
-        auto each = [&](auto&& f) {                 // of a fragment: f(h, j, e)
-#pragma unroll
-            for (int h_ = 0; h_ < 2; ++h_)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) f(h_, j, e);
-        };
-
         for (int i = 0; i < n; ++i) {
             const int c = c0 + i, st = i & 1, ph = i & 1;
             const unsigned char* stage = smem + st * Sm::kStage;
@@ -265,35 +209,10 @@ delta_tc_chain_kernel(ChainArgs args) {
                 tc::mbar_wait(&done_px, ph, ab, 4);
                 tc::tc_fence_after();
                 if (alive) {
-                    // Z as operand planes: [64 value columns][plane][token][128 bytes], swizzled
                     load_frag(x, at + cPX + tok);
                     tc::tmem_wait_ld();
-                    uint32_t w[3][2][2][2];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int a = k >> 2, j = (k >> 1) & 1, r = k & 1;
-                        uint32_t p[3];
-                        cut_planes(y[a][j][2 * r] - x[a][j][2 * r],
-                                   y[a][j][2 * r + 1] - x[a][j][2 * r + 1], p);
-#pragma unroll
-                        for (int e = 0; e < 3; ++e) w[e][a][j][r] = p[e];
-                    }
-                    unsigned char* out = reinterpret_cast<unsigned char*>(ws.Z(head, c));
-                    const int col = v0 + (lane & 3) * 8;
-#pragma unroll
-                    for (int e = 0; e < 3; ++e) {
-                        __syncwarp();
-                        stage_rows(buf_a, w[e], lane);
-                        __syncwarp();
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int t = tok + (lane >> 2) + 8 * k;
-                            if (col < D)
-                                *reinterpret_cast<uint4*>(
-                                    out + ((col >> 6) * 3 + e) * 8192 + t * 128 +
-                                    ((((col >> 3) & 7) ^ (t & 7)) << 4)) = staged_row(buf, k, lane);
-                        }
-                    }
+                    each([&](int a, int j, int e) { y[a][j][e] -= x[a][j][e]; });
+                    save_frag(ws.Z_frags(head, c), 4, 0, y, cw, lane);
                 }
             } else {
                 tc::mbar_wait(&done_px, ph, ab, 6);

@@ -97,6 +97,34 @@ __device__ __forceinline__ void load_rows_frag(Frag& x, uint32_t tile, int half,
             }
     }
 }
+// A fragment to and from the workspace: [warp][N][lane] 16-byte units, `i` below N.
+__device__ __forceinline__ void save_frag(float4* out, int units, int i, const Frag& x, int warp,
+                                          int lane) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float* p = x[k >> 1][k & 1];
+        out[(warp * units + 4 * i + k) * 32 + lane] = make_float4(p[0], p[1], p[2], p[3]);
+    }
+}
+__device__ __forceinline__ void fetch_frag(Frag& x, const float4* in, int units, int i, int warp,
+                                           int lane) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float4 p = in[(warp * units + 4 * i + k) * 32 + lane];
+        float* q = x[k >> 1][k & 1];
+        q[0] = p.x; q[1] = p.y; q[2] = p.z; q[3] = p.w;
+    }
+}
+// f(h, j, e) for each place of a fragment.
+template <typename F>
+__device__ __forceinline__ void each(F&& f) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f(h, j, e);
+}
 // Packed pairs of tokens (as [16 lanes][8 tokens][2]) to 16 rows of 64 bytes in
 // shared memory, one row a token, pieces permuted; and a thread's piece of it
 // (token lane / 4 + 8 i, columns 8 (lane % 4) ..).
@@ -231,6 +259,52 @@ __device__ __forceinline__ void mma_update(uint32_t d, uint32_t a, uint32_t tile
         for (int k = 0; k < 4; ++k)
             tc::mma_bf16_ta(d, ai + k * 8, b.at(bj + k * 2048), id, i > 0 || k > 0);
     }
+}
+
+// S^T x rows^T with rows in planes (`plane` bytes apart): the product of the
+// first planes and the products with a lower one in two accumulators.
+template <int DP, int FIRST, int LAST>
+__device__ __forceinline__ void mma_state_planes(uint32_t d_hi, uint32_t d_lo, uint32_t tm,
+                                                 uint32_t lo, uint32_t tile, int half, int plane,
+                                                 int steps) {
+    constexpr uint32_t id = tc::idesc_bf16(128, 64, false, false);
+    const Desc b(tile, 0, 1024);
+    uint32_t code = Pairs<3>::kCode;
+#pragma unroll
+    for (int n = 0; n < 6; ++n, code >>= 4) {
+        const int i = code & 3, j = (code >> 2) & 3;
+#pragma unroll
+        for (int k = FIRST; k < LAST; ++k)
+            if (k < steps)
+                tc::mma_bf16_ta(n == 5 ? d_hi : d_lo, tm + state_col<DP>(i, k, lo),
+                                b.at(j * plane + (k >> 2) * half + (k & 3) * 32), id, 1);
+    }
+}
+
+// rows^T x L, the rows (one bf16 plane, 128 columns as two blocks `half` bytes
+// apart) down the product's K and L lower triangular in three planes: token block
+// ip of the rows reaches the columns up to 16 ip + 15.
+__device__ __forceinline__ void mma_rows_lower(uint32_t d_hi, uint32_t d_lo, uint32_t rows, int half,
+                                               uint32_t tile) {
+    const Desc a(rows, half, 1024), b(tile, 0, 1024);
+#pragma unroll
+    for (int j = 2; j >= 0; --j)
+#pragma unroll
+        for (int ip = 3; ip >= 0; --ip)             // the widest first: it sets all columns
+            tc::mma_bf16(j ? d_lo : d_hi, a.at(ip * 2048), b.at(j * kTri + ip * 2048),
+                         tc::idesc_bf16(128, 16 * ip + 16, true, true), j == 1 || ip < 3);
+}
+
+// planes of A (32 columns apart, three) x rows of one plane: n columns.
+__device__ __forceinline__ void mma_planes_rows(uint32_t d, uint32_t a, uint32_t tile, int n,
+                                                bool add) {
+    const uint32_t id = tc::idesc_bf16(128, 0, false, true) | ((uint32_t)(n >> 3) << 17);
+    const Desc b(tile, 0, 1024);
+#pragma unroll
+    for (int p = 2; p >= 0; --p)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            tc::mma_bf16_ta(d, a + 32 * p + 8 * k, b.at(k * 2048), id, add || p < 2 || k > 0);
 }
 
 }  // namespace dtc

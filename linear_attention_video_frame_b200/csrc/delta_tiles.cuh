@@ -51,16 +51,35 @@ struct DeltaWs {
         w.Kt_ = take(dt == LA_BF16 ? n * 3 * w.plane_bytes() : 0);
         w.planes_ = take(dt == LA_F32 ? nk * 2 * w.NP * w.plane_bytes() : 0);
         if (backward) {
-            w.states_ = take((size_t)B * Hv * (w.chunks + 1) * w.image_bytes());
-            w.dstates_ = take(n * w.image_bytes());
-            w.Z_ = take(n * w.NP * w.plane_bytes());
-            w.dX_ = take(n * w.NP * w.plane_bytes());
+            const size_t image = dt == LA_F32 ? w.image_bytes() : w.state_frag_bytes();
+            const size_t rows = dt == LA_F32 ? w.NP * w.plane_bytes() : kRowFragBytes;
+            w.states_ = take((size_t)B * Hv * (w.chunks + 1) * image);
+            w.dstates_ = take(n * image);
+            w.Z_ = take(n * rows);
+            w.dX_ = take(n * rows);
         }
         w.bytes = at;
         return w;
     }
     __host__ __device__ size_t plane_bytes() const { return (size_t)kChunk * DP * 2; }
     __host__ __device__ size_t image_bytes() const { return (size_t)D * DP * 2 * NP; }
+    // bf16 inputs: states [128 x DP], Z and dX [128 x 64] in float32, each thread's
+    // values as its chain holds them (delta_tc.cuh)
+    static constexpr size_t kRowFragBytes = 128 * kChunk * 4;
+    __host__ __device__ size_t state_frag_bytes() const { return (size_t)128 * DP * 4; }
+    __device__ float4* state_frags(int head, int c) const {         // c = 0 .. chunks
+        return reinterpret_cast<float4*>(
+            states_ + ((size_t)head * (chunks + 1) + c) * state_frag_bytes());
+    }
+    __device__ float4* dstate_frags(int head, int c) const {
+        return reinterpret_cast<float4*>(dstates_ + at(head, c) * state_frag_bytes());
+    }
+    __device__ float4* Z_frags(int head, int c) const {
+        return reinterpret_cast<float4*>(Z_ + at(head, c) * kRowFragBytes);
+    }
+    __device__ float4* dX_frags(int head, int c) const {
+        return reinterpret_cast<float4*>(dX_ + at(head, c) * kRowFragBytes);
+    }
     __device__ size_t at(int head, int c) const { return (size_t)head * chunks + c; }
     __device__ float* gates(int head, int c) const {
         return reinterpret_cast<float*>(gates_) + at(head, c) * kGateRows * kChunk;
@@ -101,6 +120,12 @@ cudaError_t launch_delta_tc_prep(const la_delta& in, const DeltaWs& ws, bool bac
 // backward pass
 cudaError_t launch_delta_tc_chain(const la_delta& in, const DeltaWs& ws, void* o, Row3 os,
                                   float* state_out, bool states, cudaStream_t st);
+// its mirror (delta_tc_reverse.cu) and the gradients of all chunks
+// (delta_tc_grad.cu), bf16 inputs
+cudaError_t launch_delta_tc_reverse(const la_delta& in, const DeltaGrad& g, const DeltaWs& ws,
+                                    cudaStream_t st);
+cudaError_t launch_delta_tc_grad(const la_delta& in, const DeltaGrad& g, const DeltaWs& ws,
+                                 cudaStream_t st);
 // prep and forward chain of the backward pass (delta_chunk.cu)
 cudaError_t launch_delta_states(const la_delta& in, const DeltaWs& ws, cudaStream_t st);
 
