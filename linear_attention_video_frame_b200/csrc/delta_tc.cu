@@ -37,7 +37,93 @@ struct ChainArgs {
     void* o;
     Row3 os;
     float* state_out;
+    int pass;                       // 0: whole chains; 1, 2: the passes over segments
 };
+
+// The part of a head's chain that a block runs.
+struct Job {
+    int head, c0, c1;
+    bool emit;                      // outputs (or states) and the final state
+    bool identity;                  // from the identity, without values
+    const float* init;              // or NULL: zeros
+    float* last;                    // or NULL
+};
+__device__ __forceinline__ Job chain_job(const ChainArgs& a) {
+    const la_delta& in = a.in;
+    const DeltaWs& ws = a.ws;
+    const int segs = ws.seg.count, block = blockIdx.x;
+    const size_t dd = (size_t)in.D * in.D;
+    Job j{block, 0, 0, true, false, nullptr, nullptr};
+    int s = 0;
+    if (a.pass == 1) {
+        const int jobs = segs > 2 ? 2 * segs - 3 : 1, k = block % jobs;
+        j.head = block / jobs;
+        j.emit = k == 0;
+        j.identity = k > segs - 2;
+        s = j.identity ? k - (segs - 2) : k;
+    } else if (a.pass == 2) {
+        j.head = block / (segs - 1);
+        s = block % (segs - 1) + 1;
+    }
+    const int n = (seq_len(in.lengths, j.head / in.Hv, in.T) + kChunk - 1) / kChunk;
+    j.c0 = s * ws.seg.chunks;
+    j.c1 = min(n, j.c0 + ws.seg.chunks);
+    if (j.emit) {
+        j.init = s > 0 ? ws.segment(ws.seg_state, j.head, s)
+                       : in.state_in ? in.state_in + j.head * dd : nullptr;
+        if (n <= j.c0 && s > 0) j.last = nullptr;       // behind the sequence
+        else if (n <= j.c0 + ws.seg.chunks) j.last = a.state_out ? a.state_out + j.head * dd : nullptr;
+        else if (a.pass == 1) j.last = ws.segment(ws.seg_state, j.head, 1);
+    } else {
+        j.last = ws.segment(j.identity ? ws.seg_A : ws.seg_B, j.head, s);
+    }
+    if (j.c1 < j.c0) j.c1 = j.c0;
+    return j;
+}
+
+// S before segment s + 1 = A_s S + B_s, segment by segment: eight columns of a
+// head's state a block, a key row a thread.
+constexpr int kJoinCols = 8;
+__global__ void __launch_bounds__(128)
+delta_join_kernel(la_delta in, DeltaWs ws) {
+    __shared__ __align__(16) float S[128][kJoinCols];
+    const int head = blockIdx.x, v = blockIdx.y * kJoinCols, k = threadIdx.x, D = in.D;
+    const int n = (seq_len(in.lengths, head / in.Hv, in.T) + kChunk - 1) / kChunk;
+    float x[kJoinCols] = {};
+    auto row = [&](float* base, int s) { return ws.segment(base, head, s) + (size_t)k * D; };
+    if (n <= ws.seg.chunks) return;
+    if (k < D)
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) x[i] = row(ws.seg_state, 1)[v + i];
+    for (int s = 1; s + 1 < ws.seg.count && (s + 1) * ws.seg.chunks < n; ++s) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) S[k][i] = x[i];
+        __syncthreads();
+        if (k >= D) continue;
+        // the whole row is asked for at once: the loop is bound by its latency
+        const float4* A = reinterpret_cast<const float4*>(row(ws.seg_A, s));
+        float4 a[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (4 * j < D) a[j] = A[j];
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) x[i] = row(ws.seg_B, s)[v + i];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (4 * j >= D) break;
+#pragma unroll
+            for (int i = 0; i < kJoinCols; ++i) {
+                x[i] += a[j].x * S[4 * j][i];
+                x[i] += a[j].y * S[4 * j + 1][i];
+                x[i] += a[j].z * S[4 * j + 2][i];
+                x[i] += a[j].w * S[4 * j + 3][i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) row(ws.seg_state, s + 1)[v + i] = x[i];
+    }
+}
 
 template <int DP, bool STATES>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -56,10 +142,12 @@ delta_tc_chain_kernel(ChainArgs args) {
     const la_delta& in = args.in;
     const DeltaWs& ws = args.ws;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);
-    const int head = blockIdx.x, b = head / in.Hv, h = head % in.Hv, hk = h / (in.Hv / in.Hk);
+    const Job job = chain_job(args);
+    const int head = job.head, b = head / in.Hv, h = head % in.Hv, hk = h / (in.Hv / in.Hk);
     const int D = in.D;
     const int len = seq_len(in.lengths, b, in.T);
-    const int c0 = 0, c1 = (len + kChunk - 1) / kChunk, n = c1 - c0;
+    const int c0 = job.c0, c1 = job.c1, n = c1 - c0;
+    const bool emit = job.emit;
     const tc::Abort ab{&s_abort, ws.status};
 
     if (tid == 0) {
@@ -110,11 +198,11 @@ delta_tc_chain_kernel(ChainArgs args) {
                         for (int e = 0; e < 4; ++e) {
                             const int k = k0 + 16 * i + 8 * j + 2 * tq + (e & 1);
                             const int v = v0 + 16 * h + 8 * (e >> 1) + g;
-                            f(S[i][h][j][e], ((size_t)head * D + k) * D + v, k < D && v < D);
+                            f(S[i][h][j][e], (size_t)k * D + v, k < D && v < D, k == v);
                         }
         };
-        each_state([&](float& x, size_t p, bool on) {
-            x = in.state_in && on ? in.state_in[p] : 0.f;
+        each_state([&](float& x, size_t p, bool on, bool one) {
+            x = job.identity && one ? 1.f : job.init && on ? job.init[p] : 0.f;
         });
         const int cw = warp - kFirstCompute;
         auto put_state = [&](int c) {               // for the backward pass
@@ -129,7 +217,7 @@ delta_tc_chain_kernel(ChainArgs args) {
             arrive(&ready_s[side], lane);
         }
         if constexpr (STATES)
-            if (alive) put_state(c0);
+            if (alive && emit && (n > 0 || c0 == 0)) put_state(c0);
 
         // The outputs of a chunk, 16 tokens x 32 columns a warp.  They leave one chunk
         // late, while the tensor core has the chain.
@@ -155,7 +243,10 @@ delta_tc_chain_kernel(ChainArgs args) {
             tc::mbar_wait(&full[st], (i >> 1) & 1, ab, 1);
             factors(ga, gates + tok, tq);
             factors(be, gates + 2 * kChunk + tok, tq);
-            if (alive) load_rows_frag(y, smem_u32(stage) + Sm::oV, 8192, tok, v0, lane);
+            if (alive) {
+                load_rows_frag(y, smem_u32(stage) + Sm::oV, 8192, tok, v0, lane);
+                if (job.identity) each([&](int a, int j, int e) { y[a][j][e] = 0.f; });
+            }
             const float gc = gates[kChunk - 1];
 #pragma unroll
             for (int j = 0; j < 2; ++j) f[j] = make_float2(-in.k_scale * ga[j].x, -in.k_scale * ga[j].y);
@@ -171,7 +262,7 @@ delta_tc_chain_kernel(ChainArgs args) {
                 store_a(aX, 0, x);
             }
             arrive(&ready_x, lane);
-            if constexpr (!STATES) {
+            if (!STATES && emit) {
                 if (alive && i > 0) put_out(c - 1);
                 tc::mbar_wait(&done_qs, ph, ab, 5);
                 tc::tc_fence_after();
@@ -204,8 +295,11 @@ delta_tc_chain_kernel(ChainArgs args) {
             }
             if (i + 1 < n) arrive(&ready_s[side], lane);
 
-            if constexpr (STATES) {
-                if (alive) put_state(c + 1);
+            if (!emit) {
+                // only the state goes on
+            } else if constexpr (STATES) {
+                // (the next segment writes the state that it starts from)
+                if (alive && (i + 1 < n || (c + 1) * kChunk >= len)) put_state(c + 1);
                 tc::mbar_wait(&done_px, ph, ab, 4);
                 tc::tc_fence_after();
                 if (alive) {
@@ -228,31 +322,31 @@ delta_tc_chain_kernel(ChainArgs args) {
                     }
                 }
             }
-            // done_px was waited for, so the stage's last products are done as well
+            // done_upd and, for outputs, done_px were waited for: the stage's products are done
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&empty[st]);
         }
         if constexpr (!STATES)
-            if (alive && n > 0) put_out(c1 - 1);
-        if (args.state_out)
-            each_state([&](float& x, size_t p, bool on) {
-                if (on) args.state_out[p] = x;
+            if (alive && emit && n > 0) put_out(c1 - 1);
+        if (job.last)
+            each_state([&](float& x, size_t p, bool on, bool) {
+                if (on) job.last[p] = x;
             });
     } else if (warp > 0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         // ------------------------------------------------------------------ load
-        const int job = warp - 1;                       // K | V and the gates | Kt, Pt or L
-        if (job < 2) {
-            const Row3 rows3 = row3(job ? in.v_stride : in.k_stride), q3 = row3(in.q_stride);
-            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(job ? in.v : in.k) +
-                                       rows3.at(b, job ? h : hk, 0);
+        const int role = warp - 1;                      // K | V and the gates | Kt, Pt or L
+        if (role < 2) {
+            const Row3 rows3 = row3(role ? in.v_stride : in.k_stride), q3 = row3(in.q_stride);
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(role ? in.v : in.k) +
+                                       rows3.at(b, role ? h : hk, 0);
             // and half of Q's rows each
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(in.q) + q3.at(b, hk, 32 * job);
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(in.q) + q3.at(b, hk, 32 * role);
             for (int i = 0; i < n; ++i) {
                 const int c = c0 + i, st = i & 1, t0 = c * kChunk, rows = len - t0;
                 if (i >= 2) tc::mbar_wait(&empty[st], ((i >> 1) - 1) & 1, ab, 7);
                 const uint32_t sa = smem_u32(smem + st * Sm::kStage);
-                if (job == 0) {
+                if (role == 0) {
                     load_tile(sa + Sm::oKQ, Sm::kHalf, src + t0 * rows3.t, rows3.t, rows, D,
                                         lane);
                 } else {
@@ -261,15 +355,15 @@ delta_tc_chain_kernel(ChainArgs args) {
                         cp16(sa + Sm::oGates + k * 16, ws.gates(head, c) + k * 4, true);
                 }
                 if constexpr (!STATES)
-                    if (rows > 32 * job)
-                        load_tile<32>(sa + Sm::oKQ + 8192 + 4096 * job, Sm::kHalf,
-                                                q + t0 * q3.t, q3.t, rows - 32 * job, D, lane);
+                    if (emit && rows > 32 * role)
+                        load_tile<32>(sa + Sm::oKQ + 8192 + 4096 * role, Sm::kHalf,
+                                                q + t0 * q3.t, q3.t, rows - 32 * role, D, lane);
                 cp_commit();
                 if (i + 1 < n)                          // the next chunk's, towards the L2
-                    prefetch_lines(job == 0 ? ws.Kt(head, c + 1)
+                    prefetch_lines(role == 0 ? ws.Kt(head, c + 1)
                                             : reinterpret_cast<const unsigned char*>(
                                                   STATES ? ws.L(head, c + 1) : ws.P(head, c + 1)),
-                                   job == 0 ? Sm::kKt : Sm::kPt, lane);
+                                   role == 0 ? Sm::kKt : Sm::kPt, lane);
                 cp_wait<0>();
                 tc::fence_proxy_async_smem();
                 tc::mbar_arrive(&full[st]);
@@ -279,6 +373,7 @@ delta_tc_chain_kernel(ChainArgs args) {
                 if (i >= 1) tc::mbar_wait(&done_upd[kHalves - 1], (i - 1) & 1, ab, 8);
                 tc::mbar_expect_tx(&full_kt, Sm::kKt);
                 tc::bulk_load(smem + Sm::oKt, ws.Kt(head, c0 + i), Sm::kKt, &full_kt);
+                if (!emit) continue;
                 if (i >= 1) tc::mbar_wait(&done_px, (i - 1) & 1, ab, 9);
                 tc::mbar_expect_tx(&full_pt, Sm::kPt);
                 tc::bulk_load(smem + Sm::oPt, STATES ? ws.L(head, c0 + i) : ws.P(head, c0 + i),
@@ -286,7 +381,7 @@ delta_tc_chain_kernel(ChainArgs args) {
             }
             if (n > 0 && tc::aborted(ab)) {
                 tc::mbar_drain(&full_kt, (n - 1) & 1);
-                tc::mbar_drain(&full_pt, (n - 1) & 1);
+                if (emit) tc::mbar_drain(&full_pt, (n - 1) & 1);
             }
         }
     } else {
@@ -310,13 +405,13 @@ delta_tc_chain_kernel(ChainArgs args) {
                     mma_state<3, DP, 4, 8>(tm + cKS, tm, cLo, stage + Sm::oKQ, Sm::kHalf, D / 16);
                 }
                 tc::mma_commit(&done_ks);
-                if constexpr (!STATES) {
+                if (!STATES && emit) {
                     mma_state<2, DP, 0, DP / 16>(tm + cQS, tm, cLo, stage + Sm::oKQ + 8192, Sm::kHalf,
                                      D / 16);
                     tc::mma_commit(&done_qs);
                 }
                 tc::mbar_wait(&full_kt, ph, ab, 12);
-                if constexpr (!STATES) tc::mbar_wait(&done_qs, ph, ab, 16);  // it reads S
+                if (!STATES && emit) tc::mbar_wait(&done_qs, ph, ab, 16);     // it reads S
                 tc::mbar_wait(&ready_x, ph, ab, 13);
                 if (ab.raised()) break;
                 tc::tc_fence_after();
@@ -326,6 +421,7 @@ delta_tc_chain_kernel(ChainArgs args) {
                                   D - 64 * j < 64 ? D - 64 * j : 64);
                     tc::mma_commit(&done_upd[j]);
                 }
+                if (!emit) continue;
                 tc::mbar_wait(&full_pt, ph, ab, 14);
                 if (ab.raised()) break;
                 mma_lower<STATES ? 3 : 2>(tm + cPX, tm + cX, base + Sm::oPt);
@@ -350,7 +446,16 @@ cudaError_t chain(const ChainArgs& a, cudaStream_t st) {
     static_assert(bytes <= 227 * 1024, "shared memory of a block");
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<a.in.B * a.in.Hv, kThreads, bytes, st>>>(a);
+    const int heads = a.in.B * a.in.Hv, segs = a.ws.seg.count;
+    ChainArgs args = a;
+    args.pass = segs > 1 ? 1 : 0;
+    kernel<<<heads * (segs > 2 ? 2 * segs - 3 : 1), kThreads, bytes, st>>>(args);
+    if (segs == 1 || (e = cudaGetLastError()) != cudaSuccess) return segs == 1 ? cudaGetLastError() : e;
+    if (segs > 2)
+        delta_join_kernel<<<dim3(heads, a.in.D / kJoinCols), 128, 0, st>>>(a.in, a.ws);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    args.pass = 2;
+    kernel<<<heads * (segs - 1), kThreads, bytes, st>>>(args);
     return cudaGetLastError();
 }
 
@@ -358,7 +463,7 @@ cudaError_t chain(const ChainArgs& a, cudaStream_t st) {
 
 cudaError_t launch_delta_tc_chain(const la_delta& in, const DeltaWs& ws, void* o, Row3 os,
                                   float* state_out, bool states, cudaStream_t st) {
-    const ChainArgs a{in, ws, o, os, state_out};
+    const ChainArgs a{in, ws, o, os, state_out, 0};
     if (states) return in.D <= 64 ? chain<64, true>(a, st) : chain<128, true>(a, st);
     return in.D <= 64 ? chain<64, false>(a, st) : chain<128, false>(a, st);
 }

@@ -30,7 +30,82 @@ struct ReverseArgs {
     la_delta in;
     DeltaGrad grad;
     DeltaWs ws;
+    int pass;                       // 0: whole chains; 1, 2: the passes over segments
 };
+
+// The part of a head's chain that a block runs.  seg_state now holds dS behind
+// each segment.
+struct Job {
+    int head, c0, c1;
+    bool emit;                      // dS and dX of the chunks
+    const float* init;              // or NULL: zeros
+    float* last;                    // or NULL
+};
+__device__ __forceinline__ Job reverse_job(const ReverseArgs& a) {
+    const la_delta& in = a.in;
+    const DeltaWs& ws = a.ws;
+    const int segs = ws.seg.count, block = blockIdx.x;
+    const size_t dd = (size_t)in.D * in.D;
+    Job j{block, 0, 0, true, nullptr, nullptr};
+    int s = 0;
+    if (a.pass > 0) {
+        j.head = block / (segs - 1);
+        s = block % (segs - 1) + (a.pass == 1 ? 1 : 0);     // pass 1: 1 ..; pass 2: 0 .. segs - 2
+    }
+    const int n = (seq_len(in.lengths, j.head / in.Hv, in.T) + kChunk - 1) / kChunk;
+    j.c0 = s * ws.seg.chunks;
+    j.c1 = min(n, j.c0 + ws.seg.chunks);
+    const bool is_last = n <= j.c0 + ws.seg.chunks, none = s > 0 && n <= j.c0;
+    const float* outer = a.grad.dstate_out ? a.grad.dstate_out + j.head * dd : nullptr;
+    if (none || (a.pass == 2 && s > 0 && is_last)) {        // behind the sequence, or run before
+        j.c1 = j.c0;
+        j.emit = false;
+        return j;
+    }
+    j.emit = a.pass != 1 || is_last;
+    j.init = is_last ? outer : j.emit ? ws.segment(ws.seg_state, j.head, s) : nullptr;
+    if (s == 0) j.last = a.grad.dstate_in ? a.grad.dstate_in + j.head * dd : nullptr;
+    else if (a.pass == 1)
+        j.last = j.emit ? ws.segment(ws.seg_state, j.head, s - 1) : ws.segment(ws.seg_B, j.head, s);
+    return j;
+}
+
+// dS behind segment s - 1 = A_s^T dS + B'_s, from the last segment on.
+constexpr int kJoinCols = 8;
+__global__ void __launch_bounds__(128)
+delta_join_reverse_kernel(la_delta in, DeltaWs ws) {
+    __shared__ __align__(16) float S[128][kJoinCols];
+    const int head = blockIdx.x, v = blockIdx.y * kJoinCols, k = threadIdx.x, D = in.D;
+    const int n = (seq_len(in.lengths, head / in.Hv, in.T) + kChunk - 1) / kChunk;
+    const int last = (n + ws.seg.chunks - 1) / ws.seg.chunks - 1;       // segment
+    if (last < 2) return;
+    float x[kJoinCols] = {};
+    auto row = [&](float* base, int s) { return ws.segment(base, head, s) + (size_t)k * D + v; };
+    if (k < D)
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) x[i] = row(ws.seg_state, last - 1)[i];
+    for (int s = last - 1; s > 0; --s) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) S[k][i] = x[i];
+        __syncthreads();
+        if (k >= D) continue;
+        const float* A = ws.segment(ws.seg_A, head, s) + k;
+        float a[128];
+#pragma unroll
+        for (int j = 0; j < 128; ++j)
+            if (j < D) a[j] = A[(size_t)j * D];
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) x[i] = row(ws.seg_B, s)[i];
+#pragma unroll
+        for (int j = 0; j < 128; ++j)
+            if (j < D)
+#pragma unroll
+                for (int i = 0; i < kJoinCols; ++i) x[i] += a[j] * S[j][i];
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) row(ws.seg_state, s - 1)[i] = x[i];
+    }
+}
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -46,10 +121,11 @@ delta_tc_reverse_kernel(ReverseArgs args) {
     const la_delta& in = args.in;
     const DeltaWs& ws = args.ws;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);
-    const int head = blockIdx.x, b = head / in.Hv, h = head % in.Hv, hk = h / (in.Hv / in.Hk);
+    const Job job = reverse_job(args);
+    const int head = job.head, b = head / in.Hv, h = head % in.Hv, hk = h / (in.Hv / in.Hk);
     const int D = in.D;
     const int len = seq_len(in.lengths, b, in.T);
-    const int c1 = (len + kChunk - 1) / kChunk, n = c1;
+    const int c1 = job.c1, n = c1 - job.c0;
     const tc::Abort ab{&s_abort, ws.status};
 
     if (tid == 0) {
@@ -93,11 +169,11 @@ delta_tc_reverse_kernel(ReverseArgs args) {
                 each([&](int hh, int j, int e) {
                     const int k = k0 + 16 * i + 8 * j + 2 * tq + (e & 1);
                     const int v = v0 + 16 * hh + 8 * (e >> 1) + g;
-                    f(S[i][hh][j][e], ((size_t)head * D + k) * D + v, k < D && v < D);
+                    f(S[i][hh][j][e], (size_t)k * D + v, k < D && v < D);
                 });
         };
         each_state([&](float& x, size_t p, bool on) {
-            x = args.grad.dstate_out && on ? args.grad.dstate_out[p] : 0.f;
+            x = job.init && on ? job.init[p] : 0.f;
         });
         if (n > 0) {
             if (alive)
@@ -122,7 +198,7 @@ delta_tc_reverse_kernel(ReverseArgs args) {
                 store_a(aG, 0, y);
             }
             arrive(&ready_g, lane);
-            if (alive)
+            if (alive && job.emit)
 #pragma unroll
                 for (int j = 0; j < NK / 16; ++j)
                     save_frag(ws.dstate_frags(head, c), NK / 4, j, S[j], cw, lane);
@@ -140,7 +216,7 @@ delta_tc_reverse_kernel(ReverseArgs args) {
                 store_a(aW, 0, x);
             }
             arrive(&ready_w, lane);
-            if (alive) save_frag(ws.dX_frags(head, c), 4, 0, y, cw, lane);
+            if (alive && job.emit) save_frag(ws.dX_frags(head, c), 4, 0, y, cw, lane);
 
             tc::mbar_wait(&done_upd[side], ph, ab, 3);
             tc::tc_fence_after();
@@ -162,38 +238,38 @@ delta_tc_reverse_kernel(ReverseArgs args) {
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&empty[st]);
         }
-        if (args.grad.dstate_in)
+        if (job.last)
             each_state([&](float& x, size_t p, bool on) {
-                if (on) args.grad.dstate_in[p] = x;
+                if (on) job.last[p] = x;
             });
     } else if (warp > 0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         // ------------------------------------------------------------------ load
-        const int job = warp - 1;                       // K | dO and the gates | Kt and Pt
-        if (job < 2) {
-            const Row3 rows3 = row3(job ? args.grad.do_stride : in.k_stride), q3 = row3(in.q_stride);
+        const int role = warp - 1;                      // K | dO and the gates | Kt and Pt
+        if (role < 2) {
+            const Row3 rows3 = row3(role ? args.grad.do_stride : in.k_stride), q3 = row3(in.q_stride);
             const __nv_bfloat16* src =
-                static_cast<const __nv_bfloat16*>(job ? args.grad.d_o : in.k) +
-                rows3.at(b, job ? h : hk, 0);
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(in.q) + q3.at(b, hk, 32 * job);
+                static_cast<const __nv_bfloat16*>(role ? args.grad.d_o : in.k) +
+                rows3.at(b, role ? h : hk, 0);
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(in.q) + q3.at(b, hk, 32 * role);
             for (int i = 0; i < n; ++i) {
                 const int c = c1 - 1 - i, st = i & 1, t0 = c * kChunk, rows = len - t0;
                 if (i >= 2) tc::mbar_wait(&empty[st], ((i >> 1) - 1) & 1, ab, 7);
                 const uint32_t sa = smem_u32(smem + st * Sm::kStage);
-                load_tile(sa + (job ? Sm::oO : Sm::oK), 8192, src + t0 * rows3.t, rows3.t, rows, D,
+                load_tile(sa + (role ? Sm::oO : Sm::oK), 8192, src + t0 * rows3.t, rows3.t, rows, D,
                           lane);
                 // rows behind the sequence read as 0, from an address that exists
-                load_tile<32>(sa + Sm::oQ + 4096 * job, 8192,
-                              rows > 32 * job ? q + t0 * q3.t : q - 32 * job * q3.t, q3.t,
-                              rows - 32 * job, D, lane);
-                if (job)
+                load_tile<32>(sa + Sm::oQ + 4096 * role, 8192,
+                              rows > 32 * role ? q + t0 * q3.t : q - 32 * role * q3.t, q3.t,
+                              rows - 32 * role, D, lane);
+                if (role)
                     for (int k = lane; k < 3 * kChunk / 4; k += 32)
                         cp16(sa + Sm::oGates + k * 16, ws.gates(head, c) + k * 4, true);
                 cp_commit();
                 if (i + 1 < n)                          // the next chunk's, towards the L2
-                    prefetch_lines(job == 0 ? ws.Kt(head, c - 1)
+                    prefetch_lines(role == 0 ? ws.Kt(head, c - 1)
                                             : reinterpret_cast<const unsigned char*>(ws.P(head, c - 1)),
-                                   job == 0 ? Sm::kKt : Sm::kPt, lane);
+                                   role == 0 ? Sm::kKt : Sm::kPt, lane);
                 cp_wait<0>();
                 tc::fence_proxy_async_smem();
                 tc::mbar_arrive(&full[st]);
@@ -276,7 +352,16 @@ cudaError_t reverse(const ReverseArgs& a, cudaStream_t st) {
     static_assert(bytes <= 227 * 1024, "shared memory of a block");
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<a.in.B * a.in.Hv, kThreads, bytes, st>>>(a);
+    const int heads = a.in.B * a.in.Hv, segs = a.ws.seg.count;
+    ReverseArgs args = a;
+    args.pass = segs > 1 ? 1 : 0;
+    kernel<<<heads * (segs > 1 ? segs - 1 : 1), kThreads, bytes, st>>>(args);
+    if (segs == 1 || (e = cudaGetLastError()) != cudaSuccess) return segs == 1 ? cudaGetLastError() : e;
+    if (segs > 2)
+        delta_join_reverse_kernel<<<dim3(heads, a.in.D / kJoinCols), 128, 0, st>>>(a.in, a.ws);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    args.pass = 2;
+    kernel<<<heads * (segs - 1), kThreads, bytes, st>>>(args);
     return cudaGetLastError();
 }
 
@@ -284,7 +369,7 @@ cudaError_t reverse(const ReverseArgs& a, cudaStream_t st) {
 
 cudaError_t launch_delta_tc_reverse(const la_delta& in, const DeltaGrad& g, const DeltaWs& ws,
                                     cudaStream_t st) {
-    const ReverseArgs a{in, g, ws};
+    const ReverseArgs a{in, g, ws, 0};
     return in.D <= 64 ? reverse<64>(a, st) : reverse<128>(a, st);
 }
 

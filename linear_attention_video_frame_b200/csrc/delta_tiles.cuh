@@ -18,6 +18,40 @@ template <bool F32> struct Planes {
 // Per token: exp(G), exp(G_63 - G), beta, and G as the sum of two floats.
 constexpr int kGateRows = 5;
 
+// A head's chain may be cut into segments of chunks (bf16 inputs): with few heads
+// most SMs have no chain.  Segments' transitions S -> A S + B come from running
+// them on the identity without values and on zero with them.  In `segments`
+// segments, the first pass runs the first segment outright and A and B of those
+// between; the second runs the rest from their now known states.  The backward
+// pass needs only B' in its first pass, as A^T takes A's place.
+struct Segments {
+    int count, chunks;           // of a head; of a segment
+
+    // Chunk times of the passes: rounds of jobs over the SMs (one job each), and
+    // what joining the segments costs (about 10 us, three chunk times).
+    static Segments plan(int backward, int heads, int chunks) {
+        auto rounds = [](long long jobs) {
+            return (double)((jobs + kDefaultSmCount - 1) / kDefaultSmCount);
+        };
+        const double passes = backward ? 2.0 : 1.0;
+        Segments best{1, chunks};
+        double least = passes * rounds(heads) * chunks;
+        for (int s = 2; s <= 64 && s * 4 <= chunks; ++s) {
+            const int each = (chunks + s - 1) / s;
+            if ((chunks + each - 1) / each != s) continue;      // fewer segments do
+            const double forward = rounds((long long)heads * (s > 2 ? 2 * s - 3 : 1)) +
+                                   rounds((long long)heads * (s - 1));
+            const double reverse = backward ? 2.0 * rounds((long long)heads * (s - 1)) : 0.0;
+            const double cost = (forward + reverse) * each + 4.0 * passes;
+            if (cost < 0.9 * least) {
+                least = cost;
+                best = Segments{s, each};
+            }
+        }
+        return best;
+    }
+};
+
 // What the kernels of a call hand to one another.  L and P are [64][64] bf16
 // planes as shared-memory tiles (tile_at<8>, which is also the tensor core's
 // 128-byte swizzle); blocks of 16 above the diagonal hold anything.  States are images
@@ -29,6 +63,8 @@ struct DeltaWs {
     int chunks;          // per head
     int DP, D, NP;
     size_t bytes;
+    Segments seg;
+    float *seg_state, *seg_A, *seg_B;    // [head][segment][D][D], as states
 
     static DeltaWs layout(void* mem, int backward, int dt, int B, int Hk, int Hv, int T, int D) {
         DeltaWs w{};
@@ -50,6 +86,13 @@ struct DeltaWs {
         w.P_ = take(n * w.NP * 2 * kChunk * kChunk);
         w.Kt_ = take(dt == LA_BF16 ? n * 3 * w.plane_bytes() : 0);
         w.planes_ = take(dt == LA_F32 ? nk * 2 * w.NP * w.plane_bytes() : 0);
+        w.seg = dt == LA_BF16 ? Segments::plan(backward, B * Hv, w.chunks) : Segments{1, w.chunks};
+        if (w.seg.count > 1) {
+            const size_t all = (size_t)B * Hv * w.seg.count * D * D * 4;
+            w.seg_state = reinterpret_cast<float*>(take(all));
+            w.seg_A = reinterpret_cast<float*>(take(all));
+            w.seg_B = reinterpret_cast<float*>(take(all));
+        }
         if (backward) {
             const size_t image = dt == LA_F32 ? w.image_bytes() : w.state_frag_bytes();
             const size_t rows = dt == LA_F32 ? w.NP * w.plane_bytes() : kRowFragBytes;
@@ -63,6 +106,9 @@ struct DeltaWs {
     }
     __host__ __device__ size_t plane_bytes() const { return (size_t)kChunk * DP * 2; }
     __host__ __device__ size_t image_bytes() const { return (size_t)D * DP * 2 * NP; }
+    __device__ float* segment(float* base, int head, int s) const {
+        return base + ((size_t)head * seg.count + s) * D * D;
+    }
     // bf16 inputs: states [128 x DP], Z and dX [128 x 64] in float32, each thread's
     // values as its chain holds them (delta_tc.cuh)
     static constexpr size_t kRowFragBytes = 128 * kChunk * 4;

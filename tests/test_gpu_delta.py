@@ -89,6 +89,35 @@ def test_forward_ragged(Hk, Hv, lengths, dtype):
     check(end, rs, delta_bound(130), "state")
 
 
+# long sequences of few heads, whose chains are cut into segments
+@pytest.mark.parametrize("T,D,lengths", [(1601, 128, None), (64 * 33 + 7, 64, None),
+                                         (1300, 112, [1300, 70, 0, 641]),
+                                         (64 * 24, 128, [64 * 24, 64 * 6, 64 * 6 + 1, 64])])
+def test_forward_segments(T, D, lengths):
+    B = 1 if lengths is None else len(lengths)
+    assert la.la_delta_plan(False, la.LA_BF16, B, 1, 1, T, D)[1] > 2
+    x = delta_inputs(B, 1, 1, T, D, seed=T, lengths=lengths)
+    x["log_alpha"] *= 0.1                       # states that outlive a segment
+    x["log_alpha"][:, :, T // 2] = -float("inf")
+    x["log_alpha"][0, :, T // 2] = 0.0
+    o, end = _forward(x)
+    ro, rs = delta_ref(**to64(x))
+    for b, n in enumerate(lengths or [T]):
+        if n:
+            check(o[b:b + 1, :, :n], ro[b:b + 1, :, :n], delta_bound(T), "o")
+    check(end, rs, delta_bound(T), "state")
+
+
+@pytest.mark.parametrize("T,D,Hv,lengths", [(1100, 64, 2, None), (1300, 128, 1, [1300, 70, 0, 641])])
+def test_backward_segments(T, D, Hv, lengths):
+    B = 1 if lengths is None else len(lengths)
+    assert la.la_delta_plan(True, la.LA_BF16, B, 1, Hv, T, D)[1] > 4
+    x = delta_inputs(B, 1, Hv, T, D, seed=T, lengths=lengths)
+    x["log_alpha"] *= 0.1
+    got, ref = _backward(x), delta_grads_ref(x)
+    check_grads(got, ref, x, 4 * delta_bound(T))
+
+
 @pytest.mark.parametrize("T,D", [(70, 64), (200, 128), (40, 32)])
 def test_forgetting_tokens(T, D):
     """log_alpha of -inf, of the type's lowest value and of 0; beta of 0 and 1."""
