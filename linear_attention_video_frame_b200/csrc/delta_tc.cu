@@ -81,50 +81,6 @@ __device__ __forceinline__ Job chain_job(const ChainArgs& a) {
     return j;
 }
 
-// S before segment s + 1 = A_s S + B_s, segment by segment: eight columns of a
-// head's state a block, a key row a thread.
-constexpr int kJoinCols = 8;
-__global__ void __launch_bounds__(128)
-delta_join_kernel(la_delta in, DeltaWs ws) {
-    __shared__ __align__(16) float S[128][kJoinCols];
-    const int head = blockIdx.x, v = blockIdx.y * kJoinCols, k = threadIdx.x, D = in.D;
-    const int n = (seq_len(in.lengths, head / in.Hv, in.T) + kChunk - 1) / kChunk;
-    float x[kJoinCols] = {};
-    auto row = [&](float* base, int s) { return ws.segment(base, head, s) + (size_t)k * D; };
-    if (n <= ws.seg.chunks) return;
-    if (k < D)
-#pragma unroll
-        for (int i = 0; i < kJoinCols; ++i) x[i] = row(ws.seg_state, 1)[v + i];
-    for (int s = 1; s + 1 < ws.seg.count && (s + 1) * ws.seg.chunks < n; ++s) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kJoinCols; ++i) S[k][i] = x[i];
-        __syncthreads();
-        if (k >= D) continue;
-        // the whole row is asked for at once: the loop is bound by its latency
-        const float4* A = reinterpret_cast<const float4*>(row(ws.seg_A, s));
-        float4 a[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (4 * j < D) a[j] = A[j];
-#pragma unroll
-        for (int i = 0; i < kJoinCols; ++i) x[i] = row(ws.seg_B, s)[v + i];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            if (4 * j >= D) break;
-#pragma unroll
-            for (int i = 0; i < kJoinCols; ++i) {
-                x[i] += a[j].x * S[4 * j][i];
-                x[i] += a[j].y * S[4 * j + 1][i];
-                x[i] += a[j].z * S[4 * j + 2][i];
-                x[i] += a[j].w * S[4 * j + 3][i];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kJoinCols; ++i) row(ws.seg_state, s + 1)[v + i] = x[i];
-    }
-}
-
 template <int DP, bool STATES>
 __global__ void __launch_bounds__(kThreads, 1)
 delta_tc_chain_kernel(ChainArgs args) {
@@ -451,9 +407,7 @@ cudaError_t chain(const ChainArgs& a, cudaStream_t st) {
     args.pass = segs > 1 ? 1 : 0;
     kernel<<<heads * (segs > 2 ? 2 * segs - 3 : 1), kThreads, bytes, st>>>(args);
     if (segs == 1 || (e = cudaGetLastError()) != cudaSuccess) return segs == 1 ? cudaGetLastError() : e;
-    if (segs > 2)
-        delta_join_kernel<<<dim3(heads, a.in.D / kJoinCols), 128, 0, st>>>(a.in, a.ws);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (segs > 2 && (e = launch_delta_join(a.in, a.ws, false, st)) != cudaSuccess) return e;
     args.pass = 2;
     kernel<<<heads * (segs - 1), kThreads, bytes, st>>>(args);
     return cudaGetLastError();

@@ -70,43 +70,6 @@ __device__ __forceinline__ Job reverse_job(const ReverseArgs& a) {
     return j;
 }
 
-// dS behind segment s - 1 = A_s^T dS + B'_s, from the last segment on.
-constexpr int kJoinCols = 8;
-__global__ void __launch_bounds__(128)
-delta_join_reverse_kernel(la_delta in, DeltaWs ws) {
-    __shared__ __align__(16) float S[128][kJoinCols];
-    const int head = blockIdx.x, v = blockIdx.y * kJoinCols, k = threadIdx.x, D = in.D;
-    const int n = (seq_len(in.lengths, head / in.Hv, in.T) + kChunk - 1) / kChunk;
-    const int last = (n + ws.seg.chunks - 1) / ws.seg.chunks - 1;       // segment
-    if (last < 2) return;
-    float x[kJoinCols] = {};
-    auto row = [&](float* base, int s) { return ws.segment(base, head, s) + (size_t)k * D + v; };
-    if (k < D)
-#pragma unroll
-        for (int i = 0; i < kJoinCols; ++i) x[i] = row(ws.seg_state, last - 1)[i];
-    for (int s = last - 1; s > 0; --s) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kJoinCols; ++i) S[k][i] = x[i];
-        __syncthreads();
-        if (k >= D) continue;
-        const float* A = ws.segment(ws.seg_A, head, s) + k;
-        float a[128];
-#pragma unroll
-        for (int j = 0; j < 128; ++j)
-            if (j < D) a[j] = A[(size_t)j * D];
-#pragma unroll
-        for (int i = 0; i < kJoinCols; ++i) x[i] = row(ws.seg_B, s)[i];
-#pragma unroll
-        for (int j = 0; j < 128; ++j)
-            if (j < D)
-#pragma unroll
-                for (int i = 0; i < kJoinCols; ++i) x[i] += a[j] * S[j][i];
-#pragma unroll
-        for (int i = 0; i < kJoinCols; ++i) row(ws.seg_state, s - 1)[i] = x[i];
-    }
-}
-
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 delta_tc_reverse_kernel(ReverseArgs args) {
@@ -357,9 +320,7 @@ cudaError_t reverse(const ReverseArgs& a, cudaStream_t st) {
     args.pass = segs > 1 ? 1 : 0;
     kernel<<<heads * (segs > 1 ? segs - 1 : 1), kThreads, bytes, st>>>(args);
     if (segs == 1 || (e = cudaGetLastError()) != cudaSuccess) return segs == 1 ? cudaGetLastError() : e;
-    if (segs > 2)
-        delta_join_reverse_kernel<<<dim3(heads, a.in.D / kJoinCols), 128, 0, st>>>(a.in, a.ws);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (segs > 2 && (e = launch_delta_join(a.in, a.ws, true, st)) != cudaSuccess) return e;
     args.pass = 2;
     kernel<<<heads * (segs - 1), kThreads, bytes, st>>>(args);
     return cudaGetLastError();

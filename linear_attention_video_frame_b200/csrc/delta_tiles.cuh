@@ -166,6 +166,8 @@ cudaError_t launch_delta_tc_prep(const la_delta& in, const DeltaWs& ws, bool bac
 // backward pass
 cudaError_t launch_delta_tc_chain(const la_delta& in, const DeltaWs& ws, void* o, Row3 os,
                                   float* state_out, bool states, cudaStream_t st);
+// the joins between the passes over segments (delta_tc_join.cu)
+cudaError_t launch_delta_join(const la_delta& in, const DeltaWs& ws, bool reverse, cudaStream_t st);
 // its mirror (delta_tc_reverse.cu) and the gradients of all chunks
 // (delta_tc_grad.cu), bf16 inputs
 cudaError_t launch_delta_tc_reverse(const la_delta& in, const DeltaGrad& g, const DeltaWs& ws,
