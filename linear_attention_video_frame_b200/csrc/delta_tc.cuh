@@ -23,24 +23,6 @@ constexpr int kRowThreads = 64;                      // load warps 0, 1: rows; 2
 constexpr int kThreads = (kComputeWarps + kLoadWarps + 1) * 32;
 constexpr int kTri = kChunk * kChunk * 2;            // a plane of L or P
 
-// x - (the bf16 halves of p): one mixed-precision FMA each, exact where p was cut
-// from x.  (Masking the halves out first costs 12 cycles a pair and plane set
-// beside 7.)
-__device__ __forceinline__ void minus_halves(float& x0, float& x1, uint32_t p) {
-    asm("{\n\t.reg .b16 l, h, m;\n\tmov.b32 {l, h}, %2;\n\tmov.b16 m, 0xbf80;\n\t"     // -1
-        "fma.rn.f32.bf16 %0, l, m, %0;\n\tfma.rn.f32.bf16 %1, h, m, %1;\n\t}"
-        : "+f"(x0), "+f"(x1) : "r"(p));
-}
-// Planes of two floats by cutting; their sum is the float (values below 2^-110
-// lose their last bits).
-__device__ __forceinline__ void cut_planes(float x0, float x1, uint32_t (&p)[3]) {
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        p[i] = __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632);
-        if (i < 2) minus_halves(x0, x1, p[i]);
-    }
-}
-
 // A compute warp's piece of 32 lanes x 16 columns, as fragments (tc_common.cuh):
 // [16 lanes][8 columns][4].  Everything between tensor memory and registers is
 // held like this: a thread's 16 values are of 4 tokens only, V comes by

@@ -31,22 +31,30 @@ __device__ __forceinline__ uint32_t block_cols(int r, int c, int lane) {    // a
     return packed_at(r, c, (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
 }
 
-template <int DP>
+template <int DP, bool BACKWARD>
 struct PrepTc {
     static constexpr int kTile = kChunk * DP * 2;
-    // K | Q, later P | N | L | diagonal blocks of N in float32
-    static constexpr int kP3 = 3 * kPacked;
-    static constexpr int oK = 0, oP = kTile, oN = oP + (kTile > kP3 ? kTile : kP3), oL = oN + kP3,
-                         oDiag = oL + kP3, kPitch = 17;
+    // K | Q, later P | N | L.  Forward, only L's diagonal blocks are kept (one after
+    // another), so that four blocks fit an SM.  A diagonal block of N in float32 lies
+    // where the block of L comes that is made from it.
+    static constexpr int kP3 = 3 * kPacked, kPitch = 17;
+    static constexpr int oK = 0, oP = kTile, oN = oP + (kTile > kP3 ? kTile : kP3), oL = oN + kP3;
+    static constexpr int kL = BACKWARD ? kP3 : 4 * 3 * 512;
+    static constexpr int oDiag = BACKWARD ? oL + kL : oL, kDiag = BACKWARD ? 16 * kPitch * 4 : 1536;
+    static constexpr int kBytes = BACKWARD ? oDiag + 4 * kDiag : oL + kL;
     // staging of Pt (over N and L) and of half of Kt's columns (over P and N)
-    static_assert(2 * kP3 >= 3 * kTri && oL - oP >= 3 * 8192, "staging");
-    static constexpr int kBytes = oDiag + 4 * 16 * kPitch * 4;
+    static_assert(kP3 + kL >= (BACKWARD ? 3 : 2) * kTri && oL - oP >= 3 * 8192, "staging");
+    // a plane of L, and its block (r, r)
+    static constexpr int kPlaneL = BACKWARD ? kPacked : 512;
+    static __device__ __forceinline__ int block(int r) {
+        return BACKWARD ? (r * (r + 1) / 2 + r) * 512 : r * 1536;
+    }
 };
 
 template <int DP, bool BACKWARD>
-__global__ void __launch_bounds__(128, 3)
+__global__ void __launch_bounds__(128, BACKWARD ? 3 : 4)
 delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
-    using Sm = PrepTc<DP>;
+    using Sm = PrepTc<DP, BACKWARD>;
     constexpr int CH = DP / 8;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float g_hi[kChunk], g_lo[kChunk], s_beta[kChunk], s_tail[kChunk];
@@ -63,7 +71,7 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     const uint32_t base = smem_u32(smem);
     const uint32_t sK = base + Sm::oK, sQ = base + Sm::oP, sP = sQ, sN = base + Sm::oN,
                    sL = base + Sm::oL;
-    float* diag = reinterpret_cast<float*>(smem + Sm::oDiag);
+    float* diag = reinterpret_cast<float*>(smem + Sm::oDiag + warp * Sm::kDiag);
     const int g = lane >> 2, tq = lane & 3;
 
     load_rows<false, DP>(sK, in.k, row3(in.k_stride).at(b, hk, 0), in.k_stride[2], t0, len, in.D,
@@ -115,11 +123,11 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
                 n[e] = i > j + e ? k2 * E * kk[nt][2 * r + e] : 0.f;
                 p[e] = i >= j + e ? qk_scale * E * qk[nt][2 * r + e] : 0.f;
                 if ((nt >> 1) == warp)
-                    diag[(warp * 16 + (i & 15)) * Sm::kPitch + ((j + e) & 15)] = n[e];
+                    diag[(i & 15) * Sm::kPitch + ((j + e) & 15)] = n[e];
             }
             uint32_t wn[3], wp[3];
-            split_bf16<3>(n[0], n[1], wn);
-            split_bf16<3>(p[0], p[1], wp);
+            cut_planes(n[0], n[1], wn);
+            cut_planes(p[0], p[1], wp);
             const uint32_t at = packed_at(warp, nt >> 1, i & 15, nt & 1) + 4 * tq;
 #pragma unroll
             for (int e = 0; e < 3; ++e) {
@@ -131,7 +139,7 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     __syncwarp();
     // this warp's diagonal block: column `lane`
     {
-        const float* n = diag + warp * 16 * Sm::kPitch;
+        const float* n = diag;
         const int c = lane & 15;
         float l[16], bl[16];
 #pragma unroll
@@ -145,17 +153,18 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
             l[i] = i > c ? n[i * Sm::kPitch + c] - (s0 + s1) : 0.f;
             bl[i] = s_beta[warp * 16 + i] * l[i];
         }
+        __syncwarp();                 // all of the block has been read
         if (lane < 16)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float x = l[i];
+            for (int i = 0; i < 16; i += 2) {
+                uint32_t p[3];
+                cut_planes(l[i], l[i + 1], p);
 #pragma unroll
                 for (int e = 0; e < 3; ++e) {
-                    const __nv_bfloat16 w = __float2bfloat16_rn(x);
-                    *reinterpret_cast<__nv_bfloat16*>(smem + Sm::oL + e * kPacked +
-                                                      packed_at(warp, warp, i, lane >> 3) +
-                                                      (lane & 7) * 2) = w;
-                    x -= __bfloat162float(w);
+                    unsigned char* t = smem + Sm::oL + Sm::block(warp) + e * Sm::kPlaneL + (lane & 7) * 2;
+                    *reinterpret_cast<uint16_t*>(t + packed_at(0, 0, i, lane >> 3)) = (uint16_t)p[e];
+                    *reinterpret_cast<uint16_t*>(t + packed_at(0, 0, i + 1, lane >> 3)) =
+                        (uint16_t)(p[e] >> 16);
                 }
             }
     }
@@ -166,7 +175,7 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     {
         uint32_t w[3][4];
 #pragma unroll
-        for (int e = 0; e < 3; ++e) ldsm4_t(w[e], sL + e * kPacked + block_cols(warp, warp, lane));
+        for (int e = 0; e < 3; ++e) ldsm4_t(w[e], sL + Sm::block(warp) + e * Sm::kPlaneL + block_cols(0, 0, lane));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = warp * 16 + 2 * tq + (i >> 1) * 8;
@@ -177,7 +186,7 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
                 x1 += __uint_as_float(w[e][i] & 0xffff0000u);
             }
             uint32_t p[3];
-            split_bf16<3>(s_beta[t] * x0, s_beta[t + 1] * x1, p);
+            cut_planes(s_beta[t] * x0, s_beta[t + 1] * x1, p);
 #pragma unroll
             for (int e = 0; e < 3; ++e) bl[0][e][i] = p[e];
         }
@@ -222,11 +231,11 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
                 X[j][e] = be[j][e & 1] * R[j][e];
             }
         uint32_t x[3][4], l[3][4];
-        split_tiles<3>(X[0], X[1], x);
+        cut_tiles(X[0], X[1], x);
         C[0].zero();
         C[1].zero();
 #pragma unroll
-        for (int e = 0; e < 3; ++e) ldsm4(l[e], sL + e * kPacked + block_cols(r, r, lane));
+        for (int e = 0; e < 3; ++e) ldsm4(l[e], sL + Sm::block(r) + e * Sm::kPlaneL + block_cols(0, 0, lane));
         product_planes<3, 3, 3>(C, x, l);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -235,13 +244,13 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
                 R[j][e] -= C[j][e];
                 X[j][e] = be[j][e & 1] * R[j][e];
             }
-        split_tiles<3>(X[0], X[1], bl[d]);
+        cut_tiles(X[0], X[1], bl[d]);
         if constexpr (BACKWARD) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 uint32_t w[2][3];
-                split_bf16<3>(R[j][0], R[j][1], w[0]);
-                split_bf16<3>(R[j][2], R[j][3], w[1]);
+                cut_planes(R[j][0], R[j][1], w[0]);
+                cut_planes(R[j][2], R[j][3], w[1]);
 #pragma unroll
                 for (int e = 0; e < 3; ++e)
                     stsm2_t(sL + e * kPacked +
@@ -297,8 +306,13 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
             uint32_t w[2][NP];
 #pragma unroll
             for (int e = 0; e < 4; ++e) R[j][e] -= C[j][e];
-            split_bf16<NP>(R[j][0], R[j][1], w[0]);
-            split_bf16<NP>(R[j][2], R[j][3], w[1]);
+            if constexpr (NP == 3) {
+                cut_planes(R[j][0], R[j][1], w[0]);
+                cut_planes(R[j][2], R[j][3], w[1]);
+            } else {
+                split_bf16<NP>(R[j][0], R[j][1], w[0]);
+                split_bf16<NP>(R[j][2], R[j][3], w[1]);
+            }
 #pragma unroll
             for (int e = 0; e < NP; ++e)
                 stsm2_t(sN + e * kTri + tile_at<8>(i * 16 + j * 8 + (lane & 7),
@@ -313,6 +327,7 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
             reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(smem + Sm::oN)[i];
     }
 
+    __syncthreads();                  // Pt has left, P has been read: Kt is staged there
     // (B L)^T to k_scale (tail o (I - B L))^T
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
@@ -333,7 +348,7 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
                 x[e] = in.k_scale * s_tail[r * 16 + t + e] * (one - x[e]);
             }
             uint32_t p[3];
-            split_bf16<3>(x[0], x[1], p);
+            cut_planes(x[0], x[1], p);
 #pragma unroll
             for (int e = 0; e < 3; ++e) bl[d][e][i] = p[e];
         }
@@ -341,31 +356,34 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     // Kt, 64 columns at a time: rows 16 w .. 16 w + 15
 #pragma unroll 1
     for (int half = 0; half < DP / 64; ++half) {
-        Acc C[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) C[j].zero();
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const int r = warp + d;
-            if (r > 3) break;
-#pragma unroll
-            for (int np = 0; np < 4; ++np)
-                product_rows<3, 3, 1, CH>(C + 2 * np, bl[d], sK, Sm::kTile, r * 16,
-                                          half * 8 + 2 * np, lane);
-        }
-        __syncthreads();              // the staged values before have left
+        if (half > 0) __syncthreads();      // the staged values before have left
         unsigned char* stage = smem + Sm::oP;
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+            Acc C[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 4; ++j) C[j].zero();
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                uint32_t w[3];
-                split_bf16<3>(C[j][2 * r], C[j][2 * r + 1], w);
-                const uint32_t at = tile_at<8>(warp * 16 + g + 8 * r, j) + 4 * tq;
+            for (int d = 0; d < 4; ++d) {
+                const int r = warp + d;
+                if (r > 3) break;
 #pragma unroll
-                for (int e = 0; e < 3; ++e)
-                    *reinterpret_cast<uint32_t*>(stage + e * 8192 + at) = w[e];
+                for (int np = 0; np < 2; ++np)
+                    product_rows<3, 3, 1, CH>(C + 2 * np, bl[d], sK, Sm::kTile, r * 16,
+                                              half * 8 + 4 * q + 2 * np, lane);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    uint32_t w[3];
+                    cut_planes(C[j][2 * r], C[j][2 * r + 1], w);
+                    const uint32_t at = tile_at<8>(warp * 16 + g + 8 * r, 4 * q + j) + 4 * tq;
+#pragma unroll
+                    for (int e = 0; e < 3; ++e)
+                        *reinterpret_cast<uint32_t*>(stage + e * 8192 + at) = w[e];
+                }
+        }
         __syncthreads();
         unsigned char* out = ws.Kt(head, chunk) + half * 3 * 8192;
         for (int i = tid; i < 3 * 8192 / 16; i += 128)
@@ -376,7 +394,7 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
 template <int DP, bool BACKWARD>
 cudaError_t prep(const la_delta& in, const DeltaWs& ws, cudaStream_t st) {
     auto* kernel = delta_tc_prep_kernel<DP, BACKWARD>;
-    constexpr int bytes = PrepTc<DP>::kBytes;
+    constexpr int bytes = PrepTc<DP, BACKWARD>::kBytes;
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), bytes);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)(in.B * in.Hv) * (unsigned)ws.chunks, 128, bytes, st>>>(in, ws, ws.chunks);

@@ -85,6 +85,36 @@ __device__ __forceinline__ void split_tiles(const float (&c0)[4], const float (&
     }
 }
 
+// x - (the bf16 halves of p): one mixed-precision FMA each, exact where p was cut
+// from x.  (Masking the halves out first costs 12 cycles a pair and plane set
+// beside 7.)
+__device__ __forceinline__ void minus_halves(float& x0, float& x1, uint32_t p) {
+    asm("{\n\t.reg .b16 l, h, m;\n\tmov.b32 {l, h}, %2;\n\tmov.b16 m, 0xbf80;\n\t"     // -1
+        "fma.rn.f32.bf16 %0, l, m, %0;\n\tfma.rn.f32.bf16 %1, h, m, %1;\n\t}"
+        : "+f"(x0), "+f"(x1) : "r"(p));
+}
+// Planes of two floats by cutting; their sum is the float (values below 2^-110
+// lose their last bits).
+__device__ __forceinline__ void cut_planes(float x0, float x1, uint32_t (&p)[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        p[i] = __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632);
+        if (i < 2) minus_halves(x0, x1, p[i]);
+    }
+}
+
+// Two neighbouring c tiles as the three cut planes of an a operand.
+__device__ __forceinline__ void cut_tiles(const float (&c0)[4], const float (&c1)[4],
+                                          uint32_t (&a)[3][4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t p[3];
+        cut_planes(e < 2 ? c0[2 * e] : c1[2 * e - 4], e < 2 ? c0[2 * e + 1] : c1[2 * e - 3], p);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) a[i][e] = p[i];
+    }
+}
+
 // 16 bytes to shared memory; zeros when `on` is false (src is not read then).
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
