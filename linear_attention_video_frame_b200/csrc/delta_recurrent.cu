@@ -139,12 +139,128 @@ delta_recurrent_kernel(la_delta in, T* o, Row3 os, float* state_out) {
     }
 }
 
+// One token.  All of a block's state is asked for before anything else; k and q
+// come through shared memory, so that a thread holds little beside its 16 state
+// values and five blocks (80 KB of loads) are in flight on an SM.
+template <typename T, int ROWS>
+__global__ void __launch_bounds__(kThreads, ROWS > 4 ? 3 : 5)
+delta_step_kernel(la_delta in, T* o, Row3 os, float* state_out) {
+    __shared__ float4 part[kThreads / 32][kCols / 4][2];
+    __shared__ float dots[kThreads / 32];
+    __shared__ float2 kq[ROWS * kRowGroups];
+
+    const int h = blockIdx.y, b = blockIdx.z;
+    const int hk = h / (in.Hv / in.Hk);
+    const int D = in.D;
+    const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int col = blockIdx.x * kCols + cg * 4;
+    const bool live = col < D;
+    const size_t head = (size_t)b * in.Hv + h;
+    const bool on = seq_len(in.lengths, b, 1) > 0;
+    if (!on && (!state_out || state_out == in.state_in)) return;
+
+    const float* s_in = in.state_in ? in.state_in + head * D * D : nullptr;
+    float4 S[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int r = rg + i * kRowGroups;
+        S[i] = (s_in && live && r < D)
+                   ? __ldcs(reinterpret_cast<const float4*>(s_in + (size_t)r * D + col))
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (on) {
+        const T* q = static_cast<const T*>(in.q) + row3(in.q_stride).at(b, hk, 0);
+        const T* k = static_cast<const T*>(in.k) + row3(in.k_stride).at(b, hk, 0);
+        const T* v = static_cast<const T*>(in.v) + row3(in.v_stride).at(b, h, 0);
+        const float alpha = expf(in.log_alpha[head]), beta = in.beta[head];
+        if (threadIdx.x < ROWS * kRowGroups)
+            kq[threadIdx.x] = threadIdx.x < D ? make_float2(ld(k + threadIdx.x) * in.k_scale,
+                                                            ld(q + threadIdx.x) * in.q_scale)
+                                              : make_float2(0.f, 0.f);
+        float vv[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) vv[j] = live ? ld(v + col + j) : 0.f;
+        __syncthreads();
+        float4 m = make_float4(0.f, 0.f, 0.f, 0.f), p = m;
+        float qk = 0.f;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const float2 f = kq[rg + i * kRowGroups];
+            m.x += f.x * S[i].x; m.y += f.x * S[i].y;
+            m.z += f.x * S[i].z; m.w += f.x * S[i].w;
+            p.x += f.y * S[i].x; p.y += f.y * S[i].y;
+            p.z += f.y * S[i].z; p.w += f.y * S[i].w;
+            qk += f.x * f.y;
+        }
+        // the four rows of a warp that share a column group
+#pragma unroll
+        for (int d = 8; d < 32; d <<= 1) {
+            m.x += __shfl_xor_sync(~0u, m.x, d); m.y += __shfl_xor_sync(~0u, m.y, d);
+            m.z += __shfl_xor_sync(~0u, m.z, d); m.w += __shfl_xor_sync(~0u, m.w, d);
+            p.x += __shfl_xor_sync(~0u, p.x, d); p.y += __shfl_xor_sync(~0u, p.y, d);
+            p.z += __shfl_xor_sync(~0u, p.z, d); p.w += __shfl_xor_sync(~0u, p.w, d);
+            qk += __shfl_xor_sync(~0u, qk, d);
+        }
+        if (lane < 8) {
+            part[warp][cg][0] = m;
+            part[warp][cg][1] = p;
+            if (lane == 0) dots[warp] = qk;
+        }
+        __syncthreads();
+        m = p = make_float4(0.f, 0.f, 0.f, 0.f);
+        qk = 0.f;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const float4 a = part[w][cg][0];
+            m.x += a.x; m.y += a.y; m.z += a.z; m.w += a.w;
+        }
+        const float4 u = make_float4(beta * (vv[0] - alpha * m.x), beta * (vv[1] - alpha * m.y),
+                                     beta * (vv[2] - alpha * m.z), beta * (vv[3] - alpha * m.w));
+        if (rg == 0 && live) {
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) {
+                const float4 c = part[w][cg][1];
+                p.x += c.x; p.y += c.y; p.z += c.z; p.w += c.w;
+                qk += dots[w];
+            }
+            T* out = o + os.at(b, h, 0) + col;
+            st_out(out, alpha * p.x + qk * u.x);
+            st_out(out + 1, alpha * p.y + qk * u.y);
+            st_out(out + 2, alpha * p.z + qk * u.z);
+            st_out(out + 3, alpha * p.w + qk * u.w);
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const float f = kq[rg + i * kRowGroups].x;
+            S[i].x = alpha * S[i].x + f * u.x; S[i].y = alpha * S[i].y + f * u.y;
+            S[i].z = alpha * S[i].z + f * u.z; S[i].w = alpha * S[i].w + f * u.w;
+        }
+    }
+    if (!state_out) return;
+    float* s_out = state_out + head * D * D;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int r = rg + i * kRowGroups;
+        if (live && r < D) __stcs(reinterpret_cast<float4*>(s_out + (size_t)r * D + col), S[i]);
+    }
+}
+
 template <typename T>
 void launch_typed(const la_delta& in, void* o, const long long os[3], float* state_out,
                   cudaStream_t st) {
     const dim3 grid((in.D + kCols - 1) / kCols, in.Hv, in.B);
     T* out = static_cast<T*>(o);
     const Row3 r = o ? row3(os) : Row3{0, 0, 0};
+    if (in.T == 1) {
+        if (in.D <= 64)
+            delta_step_kernel<T, 2><<<grid, kThreads, 0, st>>>(in, out, r, state_out);
+        else if (in.D <= 128)
+            delta_step_kernel<T, 4><<<grid, kThreads, 0, st>>>(in, out, r, state_out);
+        else
+            delta_step_kernel<T, 8><<<grid, kThreads, 0, st>>>(in, out, r, state_out);
+        return;
+    }
     if (in.D <= 64)
         delta_recurrent_kernel<T, 2><<<grid, kThreads, 0, st>>>(in, out, r, state_out);
     else if (in.D <= 128)

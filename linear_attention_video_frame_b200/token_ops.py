@@ -12,10 +12,11 @@ contiguous float32; lengths ``[B]`` is int32 or None.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
-from . import LA_ERR_UNSUPPORTED, LaScanError, _check, _dtype_code, _ptr, _raise, _stream, lib
+from . import (LA_ERR_UNSUPPORTED, LA_OK, LaScanError, _check, _dtype_code, _raise, _stream, lib)
 
 __all__ = [
     "LaDelta", "la_gated_delta_rule", "la_gated_delta_rule_backward", "la_gated_delta_step",
@@ -37,9 +38,16 @@ class LaDelta(ctypes.Structure):
                 ("T", ctypes.c_int), ("D", ctypes.c_int)]
 
 
+# The struct and strides go over as packed bytes: a call of one token is bound by
+# what happens before its launch.
+_pack_delta = struct.Struct("3P9q4P2f6i").pack
+_pack_strides = struct.Struct("3q").pack
+assert struct.calcsize("3P9q4P2f6i") == ctypes.sizeof(LaDelta)
+
+
 def _declare():
     P, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
-    LL, S, R = ctypes.c_longlong, ctypes.POINTER(ctypes.c_longlong), ctypes.POINTER(LaDelta)
+    LL, S, R = ctypes.c_longlong, P, P
     lib.la_gated_delta_rule.argtypes = [R, P, S, P, P, Z, P]
     lib.la_gated_delta_rule.restype = I
     lib.la_gated_delta_rule_backward.argtypes = [R, P, S, P, P, P, P, P, P, P, P, Z, P]
@@ -86,48 +94,81 @@ def la_norm_workspace_size(rows: int, N: int) -> int:
     return int(lib.la_norm_workspace_size(rows, N))
 
 
-def _check_device(device: torch.device, *tensors):
-    """Kernels run on the current device: every tensor must live there."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    for name, t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-
-
-def _rows(t: torch.Tensor, name: str, shape, dtype):
-    """Checks a [B, H, T, D] tensor with contiguous rows; its strides."""
+def _here(t: torch.Tensor, name: str) -> torch.device:
+    """Kernels run on the current device, and the first tensor must live there."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
+    device = t.device
+    if device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors are on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return device
+
+
+def _raw_stream(stream, device: torch.device):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream(stream)
+
+
+def _full(t, name: str, shape, dtype, device):
+    """The address of a contiguous tensor of this shape, dtype and device; None stays None."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _check(t, name, shape, dtype)
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _space(workspace, need: int, device):
+    """A workspace's address (a new one's where None is given) and the tensor that owns it."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+    return workspace
+
+
+def _rows(t, name: str, shape, dtype, device):
+    """The strides of [..., D] rows, which are contiguous themselves.  The stride of an axis of
+    one element is never taken; torch may report any value for it."""
+    s = t.stride()
+    if t.shape != shape or t.dtype is not dtype or t.device != device or \
+            (s[-1] != 1 and shape[-1] != 1):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
         raise ValueError(f"the rows of {name} must be contiguous")
-    # the stride of an axis of one element is never taken; torch may report any value for it
-    return _Strides(*(s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape[:3])))
+    if len(shape) == 3:             # one token
+        return (s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0, 0)
+    return (s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0,
+            s[2] if shape[2] > 1 else 0)
 
 
-def _inputs(q, k, v, log_alpha, beta, k_scale, q_scale, state_in, lengths) -> LaDelta:
-    if q.dim() != 4 or v.dim() != 4:
-        raise ValueError("q, k and v are [B, H, T, D]")
-    B, Hk, T, D = q.shape
-    Hv = v.shape[1]
-    _dtype_code(q)
-    qs = _rows(q, "q", (B, Hk, T, D), q.dtype)
-    ks = _rows(k, "k", (B, Hk, T, D), q.dtype)
-    vs = _rows(v, "v", (B, Hv, T, D), q.dtype)
-    for t, n in ((log_alpha, "log_alpha"), (beta, "beta")):
-        _check(t, n, (B, Hv, T), torch.float32)
-    _check(state_in, "state_in", (B, Hv, D, D), torch.float32)
-    _check(lengths, "lengths", (B,), torch.int32)
-    _check_device(q.device, ("k", k), ("v", v), ("log_alpha", log_alpha), ("beta", beta),
-                  ("state_in", state_in), ("lengths", lengths))
-    return LaDelta(_ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(log_alpha), _ptr(beta),
-                   _ptr(state_in), _ptr(lengths), float(k_scale), float(q_scale),
-                   _dtype_code(q), B, Hk, Hv, T, D)
+def _inputs(q, k, v, log_alpha, beta, k_scale, q_scale, state_in, lengths, device):
+    """The packed la_delta; q, k, v are [B, H, T, D], or [B, H, D] with T = 1."""
+    shape, vshape = q.shape, v.shape
+    B, Hk, D = shape[0], shape[1], shape[-1]
+    Hv = vshape[1]
+    T = shape[2] if len(shape) == 4 else 1
+    dtype = q.dtype
+    code = _dtype_code(q)
+    gates, f32 = vshape[:-1], torch.float32
+    qs = _rows(q, "q", shape, dtype, device)
+    ks = _rows(k, "k", shape, dtype, device)
+    vs = _rows(v, "v", (B, Hv, T, D) if len(shape) == 4 else (B, Hv, D), dtype, device)
+    return _pack_delta(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), *qs, *ks, *vs,
+        _full(log_alpha, "log_alpha", gates, f32, device), _full(beta, "beta", gates, f32, device),
+        _full(state_in, "state_in", (B, Hv, D, D), f32, device) or 0,
+        _full(lengths, "lengths", (B,), torch.int32, device) or 0,
+        k_scale, q_scale, code, B, Hk, Hv, T, D), code
 
 
 def _new_rows(like: torch.Tensor, lengths) -> torch.Tensor:
@@ -141,20 +182,25 @@ def la_gated_delta_rule(q, k, v, log_alpha, beta, k_scale: float = 1.0, q_scale:
     """Gated delta rule over T tokens: ``S_t = alpha_t (I - beta_t k k^T) S_{t-1} + beta_t k v^T``,
     ``o_t = q S_t`` with ``alpha = exp(log_alpha)`` (see include/la_token.h).  Returns o; rows
     behind a sequence's length are left as they were in a given o, 0 in a new one."""
-    a = _inputs(q, k, v, log_alpha, beta, k_scale, q_scale, state_in, lengths)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v are [B, H, T, D]")
+    device = _here(q, "q")
+    a, code = _inputs(q, k, v, log_alpha, beta, k_scale, q_scale, state_in, lengths, device)
     B, Hv, T, D = v.shape
     if o is None:
         o = _new_rows(v, lengths)
-        if T and o.stride(2) == 0:                   # v was a broadcast view
+        if o.stride(-1) != 1 or 0 in o.stride():         # v was a broadcast view
             o = o.contiguous()
-    os = _rows(o, "o", (B, Hv, T, D), q.dtype)
-    _check(state_out, "state_out", (B, Hv, D, D), torch.float32)
-    if workspace is None:
-        workspace = delta_workspace_for(False, a.dt, B, a.Hk, Hv, T, D, q.device)
-    _check_device(q.device, ("o", o), ("state_out", state_out), ("workspace", workspace))
-    st = lib.la_gated_delta_rule(ctypes.byref(a), _ptr(o), os, _ptr(state_out), _ptr(workspace),
-                                 workspace.numel(), _stream(stream))
-    _raise(st, "la_gated_delta_rule")
+    os = _rows(o, "o", (B, Hv, T, D), q.dtype, device)
+    end = _full(state_out, "state_out", (B, Hv, D, D), torch.float32, device)
+    need = lib.la_delta_workspace_size(0, code, B, q.shape[1], Hv, T, D)
+    if need == 0:
+        raise LaScanError(LA_ERR_UNSUPPORTED, "la_gated_delta_rule")
+    workspace = _space(workspace, need, device)
+    st = lib.la_gated_delta_rule(a, o.data_ptr(), _pack_strides(*os), end, workspace.data_ptr(),
+                                 workspace.numel(), _raw_stream(stream, device))
+    if st != LA_OK:
+        _raise(st, "la_gated_delta_rule")
     return o
 
 
@@ -165,22 +211,23 @@ def la_gated_delta_step(q, k, v, log_alpha, beta, state_in, k_scale: float = 1.0
     the new state.  A sequence of length 0 keeps its state and its row of o."""
     if q.dim() != 3 or v.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v of a step are [B, H, D]")
-    B, Hv, D = v.shape
-    _check(log_alpha, "log_alpha", (B, Hv), torch.float32)
-    _check(beta, "beta", (B, Hv), torch.float32)
-    if o is None:
-        o = _new_rows(v, lengths)
     if state_out is None:
         state_out = state_in
     if state_out is None:
         raise ValueError("a step needs state_in or state_out")
-    a = _inputs(q.unsqueeze(2), k.unsqueeze(2), v.unsqueeze(2), log_alpha.unsqueeze(2),
-                beta.unsqueeze(2), k_scale, q_scale, state_in, lengths)
-    os = _rows(o.unsqueeze(2), "o", (B, Hv, 1, D), q.dtype)
-    _check(state_out, "state_out", (B, Hv, D, D), torch.float32)
-    _check_device(q.device, ("o", o), ("state_out", state_out))
-    st = lib.la_gated_delta_step(ctypes.byref(a), _ptr(o), os, _ptr(state_out), _stream(stream))
-    _raise(st, "la_gated_delta_step")
+    device = _here(q, "q")
+    a, _ = _inputs(q, k, v, log_alpha, beta, k_scale, q_scale, state_in, lengths, device)
+    B, Hv, D = shape = v.shape
+    if o is None:
+        o = _new_rows(v, lengths)
+        if o.stride(-1) != 1 or 0 in o.stride():
+            o = o.contiguous()
+    os = _rows(o, "o", shape, q.dtype, device)
+    end = _full(state_out, "state_out", (B, Hv, D, D), torch.float32, device)
+    st = lib.la_gated_delta_step(a, o.data_ptr(), _pack_strides(*os), end,
+                                 _raw_stream(stream, device))
+    if st != LA_OK:
+        _raise(st, "la_gated_delta_step")
     return o
 
 
@@ -191,32 +238,34 @@ def la_gated_delta_rule_backward(q, k, v, log_alpha, beta, do, k_scale: float = 
     """Gradients (dq, dk, dv, dlog_alpha, dbeta) of la_gated_delta_rule for the gradient `do` of
     its output and `dstate_out` of its final state; dstate_in (if given) gets the initial
     state's.  Gradients of rows behind a sequence's length are 0."""
-    a = _inputs(q, k, v, log_alpha, beta, k_scale, q_scale, state_in, lengths)
-    B, Hv, T, D = v.shape
-    dos = _rows(do, "do", (B, Hv, T, D), q.dtype)
-    for t, n in ((dstate_out, "dstate_out"), (dstate_in, "dstate_in")):
-        _check(t, n, (B, Hv, D, D), torch.float32)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v are [B, H, T, D]")
+    device = _here(q, "q")
+    a, code = _inputs(q, k, v, log_alpha, beta, k_scale, q_scale, state_in, lengths, device)
+    B, Hv, T, D = vshape = v.shape
+    kshape, dtype, f32 = q.shape, q.dtype, torch.float32
+    dos = _rows(do, "do", vshape, dtype, device)
 
-    def out(t, name, shape, dtype):
-        if t is None:
-            return torch.empty(shape, dtype=dtype, device=q.device)
-        _check(t, name, shape, dtype)
-        return t
+    def out(t, shape, dt):
+        return torch.empty(shape, dtype=dt, device=device) if t is None else t
 
-    dq, dk = out(dq, "dq", q.shape, q.dtype), out(dk, "dk", k.shape, q.dtype)
-    dv = out(dv, "dv", v.shape, q.dtype)
-    dlog_alpha = out(dlog_alpha, "dlog_alpha", (B, Hv, T), torch.float32)
-    dbeta = out(dbeta, "dbeta", (B, Hv, T), torch.float32)
-    if workspace is None:
-        workspace = delta_workspace_for(True, a.dt, B, a.Hk, Hv, T, D, q.device)
-    _check_device(q.device, ("do", do), ("dstate_out", dstate_out), ("dstate_in", dstate_in),
-                  ("dq", dq), ("dk", dk), ("dv", dv), ("dlog_alpha", dlog_alpha),
-                  ("dbeta", dbeta), ("workspace", workspace))
-    st = lib.la_gated_delta_rule_backward(ctypes.byref(a), _ptr(do), dos, _ptr(dstate_out),
-                                          _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dlog_alpha),
-                                          _ptr(dbeta), _ptr(dstate_in), _ptr(workspace),
-                                          workspace.numel(), _stream(stream))
-    _raise(st, "la_gated_delta_rule_backward")
+    dq, dk, dv = out(dq, kshape, dtype), out(dk, kshape, dtype), out(dv, vshape, dtype)
+    dlog_alpha, dbeta = out(dlog_alpha, vshape[:3], f32), out(dbeta, vshape[:3], f32)
+    need = lib.la_delta_workspace_size(1, code, B, kshape[1], Hv, T, D)
+    if need == 0:
+        raise LaScanError(LA_ERR_UNSUPPORTED, "la_gated_delta_rule_backward")
+    workspace = _space(workspace, need, device)
+    st = lib.la_gated_delta_rule_backward(
+        a, do.data_ptr(), _pack_strides(*dos),
+        _full(dstate_out, "dstate_out", (B, Hv, D, D), f32, device),
+        _full(dq, "dq", kshape, dtype, device), _full(dk, "dk", kshape, dtype, device),
+        _full(dv, "dv", vshape, dtype, device),
+        _full(dlog_alpha, "dlog_alpha", vshape[:3], f32, device),
+        _full(dbeta, "dbeta", vshape[:3], f32, device),
+        _full(dstate_in, "dstate_in", (B, Hv, D, D), f32, device),
+        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, device))
+    if st != LA_OK:
+        _raise(st, "la_gated_delta_rule_backward")
     return dq, dk, dv, dlog_alpha, dbeta
 
 
@@ -226,29 +275,27 @@ def la_add_rms_norm_fp8(x, residual, weight, eps: float = 1e-6, group: int = 128
     None), weight ``[N]`` float32.  Returns (y float8_e4m3fn ``[..., N]``, scale float32
     ``[..., ceil(N / group)]`` (group = 0: ``[..., 1]``), h = x + residual as stored, which is x
     itself without a residual).  ``y.float() * scale`` (each scale over its group) is the norm."""
-    N = x.shape[-1]
+    shape, dtype = x.shape, x.dtype
+    N = shape[-1]
     dt = _dtype_code(x)
-    _check(x, "x")
-    _check(residual, "residual", x.shape, x.dtype)
-    _check(weight, "weight", (N,), torch.float32)
     if group not in (0, 128):
         raise ValueError(f"group must be 128 or 0 (the row), got {group}")
-    rows = x.numel() // N if N else 0
+    device = _here(x, "x")
+    groups = (*shape[:-1], -(-N // group) if group else 1)
     if h is None and residual is not None:
         h = torch.empty_like(x)
     if y is None:
-        y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        y = torch.empty(shape, dtype=torch.float8_e4m3fn, device=device)
     if scale is None:
-        scale = torch.empty((*x.shape[:-1], -(-N // group) if group else 1),
-                            dtype=torch.float32, device=x.device)
-    _check(h, "h", x.shape, x.dtype)
-    _check(y, "y", x.shape, torch.float8_e4m3fn)
-    _check(scale, "scale", (*x.shape[:-1], -(-N // group) if group else 1), torch.float32)
-    _check_device(x.device, ("residual", residual), ("weight", weight), ("h", h), ("y", y),
-                  ("scale", scale))
-    st = lib.la_add_rms_norm_fp8(_ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y),
-                                 _ptr(scale), dt, rows, N, group, float(eps), _stream(stream))
-    _raise(st, "la_add_rms_norm_fp8")
+        scale = torch.empty(groups, dtype=torch.float32, device=device)
+    st = lib.la_add_rms_norm_fp8(
+        _full(x, "x", shape, dtype, device), _full(residual, "residual", shape, dtype, device),
+        _full(weight, "weight", (N,), torch.float32, device), _full(h, "h", shape, dtype, device),
+        _full(y, "y", shape, torch.float8_e4m3fn, device),
+        _full(scale, "scale", groups, torch.float32, device), dt, x.numel() // N if N else 0, N,
+        group, eps, _raw_stream(stream, device))
+    if st != LA_OK:
+        _raise(st, "la_add_rms_norm_fp8")
     return y, scale, x if h is None else h
 
 
@@ -258,30 +305,27 @@ def la_add_rms_norm_backward(dy, h, weight, dh=None, eps: float = 1e-6, dx=None,
     rounding passed straight through), h as the forward pass returned it and `dh`, the gradient
     that h gets from elsewhere.  dx is the gradient of x and of residual alike; dweight is None
     when need_dweight is False."""
-    N = h.shape[-1]
+    shape, dtype = h.shape, h.dtype
+    N = shape[-1]
     dt = _dtype_code(h)
-    _check(h, "h")
-    _check(dy, "dy", h.shape, h.dtype)
-    _check(dh, "dh", h.shape, h.dtype)
-    _check(weight, "weight", (N,), torch.float32)
+    device = _here(h, "h")
     rows = h.numel() // N if N else 0
     if dx is None:
         dx = torch.empty_like(h)
-    _check(dx, "dx", h.shape, h.dtype)
+    space, size = None, 0
     if need_dweight:
         if dweight is None:
-            dweight = torch.empty((N,), dtype=torch.float32, device=h.device)
-        _check(dweight, "dweight", (N,), torch.float32)
-        if workspace is None:
-            workspace = torch.empty(la_norm_workspace_size(rows, N), dtype=torch.uint8,
-                                    device=h.device)
+            dweight = torch.empty((N,), dtype=torch.float32, device=device)
+        workspace = _space(workspace, lib.la_norm_workspace_size(rows, N), device)
+        space, size = workspace.data_ptr(), workspace.numel()
     else:
-        dweight = workspace = None
-    _check_device(h.device, ("dy", dy), ("dh", dh), ("weight", weight), ("dx", dx),
-                  ("dweight", dweight), ("workspace", workspace))
-    st = lib.la_add_rms_norm_backward(_ptr(dy), _ptr(h), _ptr(weight), _ptr(dh), _ptr(dx),
-                                      _ptr(dweight), dt, rows, N, float(eps), _ptr(workspace),
-                                      0 if workspace is None else workspace.numel(),
-                                      _stream(stream))
-    _raise(st, "la_add_rms_norm_backward")
+        dweight = None
+    st = lib.la_add_rms_norm_backward(
+        _full(dy, "dy", shape, dtype, device), _full(h, "h", shape, dtype, device),
+        _full(weight, "weight", (N,), torch.float32, device), _full(dh, "dh", shape, dtype, device),
+        _full(dx, "dx", shape, dtype, device),
+        _full(dweight, "dweight", (N,), torch.float32, device), dt, rows, N, eps, space, size,
+        _raw_stream(stream, device))
+    if st != LA_OK:
+        _raise(st, "la_add_rms_norm_backward")
     return dx, dweight
