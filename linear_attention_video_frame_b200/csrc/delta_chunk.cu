@@ -587,11 +587,12 @@ size_t delta_workspace_bytes(int backward, int dt, int B, int Hk, int Hv, int T,
 
 // prep, the chain (a chain over segments is two passes with a join between them)
 // and, in the backward pass, the reverse chain and the gradients
-int delta_kernel_count(int backward, int dt, int B, int Hv, int T) {
+int delta_kernel_count(int backward, int dt, int B, int Hk, int Hv, int T) {
     const int chunks = (T + kChunk - 1) / kChunk;
     const int segs = dt == LA_BF16 ? Segments::plan(backward, B * Hv, chunks).count : 1;
     const int chain = segs > 2 ? 3 : segs;
-    return backward ? (chunks ? 2 * chain + 2 : 1) : 1 + chain;
+    const int shares = dt == LA_BF16 && Hv > Hk ? 1 : 0;      // dq and dk added up
+    return backward ? (chunks ? 2 * chain + 2 + shares : 1) : 1 + chain;
 }
 
 cudaError_t launch_delta_chunked(const la_delta& in, void* o, const long long o_stride[3],

@@ -1,8 +1,9 @@
 // The gradients of all chunks on tcgen05 (bf16 inputs), from the states S0, Z, dS
 // and dX that the two chains left; the formulas are in delta_grad.cu.
 //
-// A block takes one chunk of one key head and adds up the value heads that share
-// it, in their order.  Its warps hold fragments as the chains did.  Products, transposed where they
+// A block takes one chunk of one value head.  Where value heads share a key head,
+// dq and dk leave in float32 and delta_share_kernel adds them up in their order.
+// The warps hold fragments as the chains did.  Products, transposed where they
 // are of key rows:
 //   rows (dO | dX) Z^T     [tokens, 2 x 64 lanes] x [64 tokens]
 //   S0 dO^T, S0 dX^T, dS Z^T, K^T dP', Q^T dP'^T, K^T (N' + N'^T)   [128 key rows] x [64 tokens]
@@ -134,7 +135,7 @@ __device__ __forceinline__ float sum_rows(float x) {
     return x;
 }
 
-// SHARED: several value heads share the key head.
+// SHARED: several value heads share a key head.
 template <int DP, bool SHARED>
 __global__ void __launch_bounds__(kGradThreads, 2)
 delta_tc_grad_kernel(GradArgs args) {
@@ -151,27 +152,34 @@ delta_tc_grad_kernel(GradArgs args) {
     const DeltaGrad& grad = args.grad;
     const DeltaWs& ws = args.ws;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);
-    const int chunk = blockIdx.x % args.chunks, khead = blockIdx.x / args.chunks;
-    const int b = khead / in.Hk, hk = khead % in.Hk, ratio = SHARED ? in.Hv / in.Hk : 1, D = in.D;
+    const int chunk = blockIdx.x % args.chunks, head = blockIdx.x / args.chunks;
+    const int b = head / in.Hv, h = head % in.Hv, hk = SHARED ? h / (in.Hv / in.Hk) : h, D = in.D;
     const int len = seq_len(in.lengths, b, in.T);
     const int t0 = chunk * kChunk, rows = in.T - t0 < kChunk ? in.T - t0 : kChunk;
     const int on = len - t0 < rows ? (len > t0 ? len - t0 : 0) : rows;   // rows of the sequence
-    const size_t out_row = (size_t)khead * in.T + t0;
+    const size_t row = (size_t)head * in.T + t0;
 
     if (on == 0) {                              // behind the sequence
         const uint4 zero = make_uint4(0, 0, 0, 0);
-        for (int rep = 0; rep < ratio; ++rep) {
-            const size_t row = ((size_t)b * in.Hv + hk * ratio + rep) * in.T + t0;
-            for (int i = tid; i < rows; i += kGradThreads)
-                grad.dlog_alpha[row + i] = grad.dbeta[row + i] = 0.f;
-            for (int i = tid; i < rows * D / 8; i += kGradThreads)
-                reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(grad.dv) + row * D)[i] = zero;
-        }
+        for (int i = tid; i < rows; i += kGradThreads)
+            grad.dlog_alpha[row + i] = grad.dbeta[row + i] = 0.f;
         for (int i = tid; i < rows * D / 8; i += kGradThreads) {
-            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(grad.dq) + out_row * D)[i] = zero;
-            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(grad.dk) + out_row * D)[i] = zero;
+            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(grad.dv) + row * D)[i] = zero;
+            if (SHARED) continue;               // delta_share_kernel's
+            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(grad.dq) + row * D)[i] = zero;
+            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(grad.dk) + row * D)[i] = zero;
         }
         return;
+    }
+    // What is read later, towards the L2: the reads follow one another.
+    {
+        const void* from[3] = {ws.state_frags(head, chunk), ws.dstate_frags(head, chunk),
+                               ws.state_frags(head, chunk + 1)};
+        const int each_bytes = (int)ws.state_frag_bytes() / kGradWarps;
+        const int warp_at = (tid >> 5) * each_bytes;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            prefetch_lines(static_cast<const char*>(from[i]) + warp_at, each_bytes, tid & 31);
     }
 
     const tc::Abort ab{&s_abort, ws.status};
@@ -239,18 +247,9 @@ delta_tc_grad_kernel(GradArgs args) {
         }
     };
 
-    Frag dq[2], dk[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        each([&](int a, int j, int e) { dq[i][a][j][e] = dk[i][a][j][e] = 0.f; });
-
-#pragma unroll 1
-    for (int rep = 0; rep < ratio; ++rep) {
-        const int h = hk * ratio + rep, head = b * in.Hv + h;
-        const size_t row = (size_t)head * in.T + t0;
-        if (SHARED) __syncthreads();            // the last head's tiles and sums have been read
-        for (int i = tid; i < kGateRows * kChunk; i += kGradThreads)
-            (&gates[0][0])[i] = ws.gates(head, chunk)[i];
+    for (int i = tid; i < kGateRows * kChunk; i += kGradThreads)
+        (&gates[0][0])[i] = ws.gates(head, chunk)[i];
+    {
         float xz[2][2] = {}, xv[2][2] = {}, cross = 0.f;
 
 #pragma unroll 1
@@ -430,8 +429,9 @@ delta_tc_grad_kernel(GradArgs args) {
             each([&](int a, int j, int e) {
                 if (j0 > i0 + 16 * a) return;   // above the diagonal: not read
                 const int ti = i0 + 16 * a + 8 * (e >> 1) + g, tj = j0 + 8 * j + 2 * tq + (e & 1);
-                // above the diagonal E may overflow: it is selected away
-                const float E = expf((gates[3][ti] - gates[3][tj]) + (gates[4][ti] - gates[4][tj])) *
+                // above the diagonal E may overflow: it is selected away.  The short
+                // exponential's error, 2^-22 and 2^-24 of the exponent, is the products'.
+                const float E = __expf((gates[3][ti] - gates[3][tj]) + (gates[4][ti] - gates[4][tj])) *
                                 gates[2][tj];
                 if (quarter < 2) p[a][j][e] = ti >= tj ? E * p[a][j][e] : 0.f;
                 else p[a][j][e] = ti > tj ? -gates[2][ti] * E * p[a][j][e] : 0.f;
@@ -448,6 +448,7 @@ delta_tc_grad_kernel(GradArgs args) {
                 for (int e = 0; e < 2; ++e) put_rows(base + Sm::oN + e * kTri, w[e], i0, j0, lane);
             }
         }
+        Frag dk[2];
         if (alive)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -461,8 +462,8 @@ delta_tc_grad_kernel(GradArgs args) {
                 load_frag(y, at + cDS + j0);
                 tc::tmem_wait_ld();
                 each([&](int a, int j, int e) {
-                    dk[i][a][j][e] += factor(be, j, e) * (factor(ta, j, e) * y[a][j][e] -
-                                                          factor(ga, j, e) * x[a][j][e]);
+                    dk[i][a][j][e] = factor(be, j, e) * (factor(ta, j, e) * y[a][j][e] -
+                                                         factor(ga, j, e) * x[a][j][e]);
                 });
             }
         cp_wait<0>();
@@ -493,15 +494,33 @@ delta_tc_grad_kernel(GradArgs args) {
                 tc::tmem_wait_ld();
                 each([&](int a, int j, int e) {
                     x[a][j][e] = factor(ga, j, e) * x[a][j][e] + in.k_scale * y[a][j][e];
-                    dq[i][a][j][e] += x[a][j][e];
                     if (quarter * 32 + 16 * a < D) qdq[j][e & 1] += q[a][j][e] * x[a][j][e];
                 });
-                load_frag(x, at + cPQ + j0);
+                Frag z;
+                load_frag(z, at + cPQ + j0);
                 load_frag(y, at + cNK + j0);
                 tc::tmem_wait_ld();
                 each([&](int a, int j, int e) {
-                    dk[i][a][j][e] += in.q_scale * x[a][j][e] + in.k_scale * y[a][j][e];
+                    x[a][j][e] *= in.q_scale;
+                    z[a][j][e] = in.k_scale * (dk[i][a][j][e] + in.q_scale * z[a][j][e] +
+                                               in.k_scale * y[a][j][e]);
                 });
+                if (SHARED) {
+                    float* pq = ws.dq_shares + row * D;
+                    float* pk = ws.dk_shares + row * D;
+                    each([&](int a, int j, int e) {
+                        const int t = j0 + 8 * j + 2 * tq + (e & 1);
+                        const int key = quarter * 32 + 16 * a + 8 * (e >> 1) + g;
+                        if (t < on && key < D) {
+                            pq[(size_t)t * D + key] = x[a][j][e];
+                            pk[(size_t)t * D + key] = z[a][j][e];
+                        }
+                    });
+                } else {
+                    unsigned char* buf = smem + warp * 1024;
+                    put_out(buf, static_cast<__nv_bfloat16*>(grad.dq) + row * D, x, quarter * 32, j0);
+                    put_out(buf, static_cast<__nv_bfloat16*>(grad.dk) + row * D, z, quarter * 32, j0);
+                }
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -511,9 +530,7 @@ delta_tc_grad_kernel(GradArgs args) {
                     if (g == 0) s_qdq[quarter][j0 + 8 * j + 2 * tq + e] = in.q_scale * s;
                 }
         }
-        tc::tc_fence_before();                  // read before the next head's products
         __syncthreads();
-        tc::tc_fence_after();
         if (warp == 0) {                        // dG, summed from the chunk's end
             double s[2];
 #pragma unroll
@@ -543,18 +560,6 @@ delta_tc_grad_kernel(GradArgs args) {
             }
         }
     }
-    if (alive)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            each([&](int a, int j, int e) {
-                dq[i][a][j][e] *= in.q_scale;
-                dk[i][a][j][e] *= in.k_scale;
-            });
-            unsigned char* buf = smem + warp * 1024;
-            const int j0 = pair * 32 + i * 16;
-            put_out(buf, static_cast<__nv_bfloat16*>(grad.dq) + out_row * D, dq[i], quarter * 32, j0);
-            put_out(buf, static_cast<__nv_bfloat16*>(grad.dk) + out_row * D, dk[i], quarter * 32, j0);
-        }
     if (warp == 0 && tc::elect_one() && tc::aborted(ab))
         for (int i = 0; i < 2; ++i) tc::mbar_drain(&done[i], phase[i] ^ 1);
     tc::tc_fence_before();
@@ -565,6 +570,33 @@ delta_tc_grad_kernel(GradArgs args) {
     }
 }
 
+// dq and dk of the key heads: the sums of their value heads', four columns a thread.
+__global__ void __launch_bounds__(256)
+delta_share_kernel(GradArgs args) {
+    const la_delta& in = args.in;
+    const int D = in.D, ratio = in.Hv / in.Hk;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, row = i / (D / 4);
+    const int c = (int)(i % (D / 4)) * 4;
+    const long long khead = row / in.T;
+    const int t = (int)(row % in.T), b = (int)(khead / in.Hk), hk = (int)(khead % in.Hk);
+    if (b >= in.B) return;
+    float4 q = make_float4(0.f, 0.f, 0.f, 0.f), k = q;
+    if (t < seq_len(in.lengths, b, in.T))
+        for (int r = 0; r < ratio; ++r) {
+            const size_t at =
+                (((size_t)b * in.Hv + hk * ratio + r) * in.T + t) * D + c;
+            const float4 x = *reinterpret_cast<const float4*>(args.ws.dq_shares + at);
+            const float4 y = *reinterpret_cast<const float4*>(args.ws.dk_shares + at);
+            q.x += x.x; q.y += x.y; q.z += x.z; q.w += x.w;
+            k.x += y.x; k.y += y.y; k.z += y.z; k.w += y.w;
+        }
+    const size_t out = (size_t)row * D + c;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(args.grad.dq) + out) =
+        make_uint2(pack_bf16(q.x, q.y), pack_bf16(q.z, q.w));
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(args.grad.dk) + out) =
+        make_uint2(pack_bf16(k.x, k.y), pack_bf16(k.z, k.w));
+}
+
 template <int DP, bool SHARED>
 cudaError_t gradients(const GradArgs& a, cudaStream_t st) {
     auto* kernel = delta_tc_grad_kernel<DP, SHARED>;
@@ -572,7 +604,10 @@ cudaError_t gradients(const GradArgs& a, cudaStream_t st) {
     static_assert(bytes <= 108 * 1024, "shared memory of two blocks");
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(a.in.B * a.in.Hk) * (unsigned)a.chunks, kGradThreads, bytes, st>>>(a);
+    kernel<<<(unsigned)(a.in.B * a.in.Hv) * (unsigned)a.chunks, kGradThreads, bytes, st>>>(a);
+    if (!SHARED || (e = cudaGetLastError()) != cudaSuccess) return SHARED ? e : cudaGetLastError();
+    const long long units = (long long)a.in.B * a.in.Hk * a.in.T * (a.in.D / 4);
+    delta_share_kernel<<<(unsigned)((units + 255) / 256), 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 

@@ -65,6 +65,7 @@ struct DeltaWs {
     size_t bytes;
     Segments seg;
     float *seg_state, *seg_A, *seg_B;    // [head][segment][D][D], as states
+    float *dq_shares, *dk_shares;        // [B, Hv, T, D], where value heads share a key head
 
     static DeltaWs layout(void* mem, int backward, int dt, int B, int Hk, int Hv, int T, int D) {
         DeltaWs w{};
@@ -98,6 +99,11 @@ struct DeltaWs {
             const size_t rows = dt == LA_F32 ? w.NP * w.plane_bytes() : kRowFragBytes;
             w.states_ = take((size_t)B * Hv * (w.chunks + 1) * image);
             w.dstates_ = take(n * image);
+            if (dt == LA_BF16 && Hv > Hk) {
+                const size_t all = (size_t)B * Hv * T * D * 4;
+                w.dq_shares = reinterpret_cast<float*>(take(all));
+                w.dk_shares = reinterpret_cast<float*>(take(all));
+            }
             w.Z_ = take(n * rows);
             w.dX_ = take(n * rows);
         }

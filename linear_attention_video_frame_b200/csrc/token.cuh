@@ -40,7 +40,7 @@ cudaError_t launch_delta_recurrent(const la_delta& in, void* o, const long long 
 // Chunked tensor-core path (delta_chunk.cu).
 bool delta_chunked(int backward, int T, int D);
 size_t delta_workspace_bytes(int backward, int dt, int B, int Hk, int Hv, int T, int D);
-int delta_kernel_count(int backward, int dt, int B, int Hv, int T);
+int delta_kernel_count(int backward, int dt, int B, int Hk, int Hv, int T);
 cudaError_t launch_delta_chunked(const la_delta& in, void* o, const long long o_stride[3],
                                  float* state_out, void* ws, cudaStream_t st);
 cudaError_t launch_delta_backward(const la_delta& in, const DeltaGrad& g, void* ws,

@@ -166,7 +166,7 @@ extern "C" const char* la_delta_plan(int backward, la_dtype dt, int B, int Hk, i
                                      int D, int* kernels) {
     if (la_delta_workspace_size(backward, dt, B, Hk, Hv, T, D) == 0) return nullptr;
     const bool chunked = delta_chunked(backward, T, D);
-    if (kernels) *kernels = chunked ? delta_kernel_count(backward, dt, B, Hv, T) : 1;
+    if (kernels) *kernels = chunked ? delta_kernel_count(backward, dt, B, Hk, Hv, T) : 1;
     return chunked ? "delta_chunked" : "delta_recurrent";
 }
 
