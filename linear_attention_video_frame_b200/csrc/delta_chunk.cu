@@ -1,4 +1,5 @@
-// Gated delta rule in chunks of 64 tokens on tensor cores.
+// Gated delta rule in chunks of 64 tokens: the mathematics, and the kernels for
+// float32 inputs on warp-level products (bf16: delta_tc_prep.cu, delta_tc.cu).
 //
 // Within a chunk that starts from state S0, with G_i the sum of log_alpha up
 // to token i, gamma_i = exp(G_i), E_ij = exp(G_i - G_j), B = diag(beta), every
@@ -24,12 +25,11 @@ namespace {
 // column a lane, 120 steps), then block column c by warp c from the top,
 //     R = N_rc - sum_j N_rj (B L_jc),   L_rc = R - L_rr (B R),
 // on tensor cores, transposed so that a block's result tiles are the next
-// product's a operand.  The serial part is 16 rows in place of 64; a column of
-// 64 rows a thread took 2.2 times as long (70 us for 2048 chunks of 128).
-template <bool F32, int DP>
+// product's a operand; the serial part is 16 rows in place of 64.
+template <int DP>
 struct PrepSmem {
     static constexpr int kTile = kChunk * DP * 2, kTri = kChunk * kChunk * 2;
-    static constexpr int NI = Planes<F32>::kInput, NP = Planes<F32>::kSplit;
+    static constexpr int NI = kPlanes, NP = kPlanes;
     // K and Q, later P, later L; N; the diagonal blocks of N in float32
     static constexpr int kQ = NI * kTile;
     static constexpr int kKQ = 2 * kQ > NP * kTri ? 2 * kQ : NP * kTri;
@@ -37,10 +37,10 @@ struct PrepSmem {
     static constexpr int kBytes = kDiag + 4 * 16 * kPitch * 4;
 };
 
-template <bool F32, int DP>
+template <int DP>
 __global__ void __launch_bounds__(128)
 delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
-    using Sm = PrepSmem<F32, DP>;
+    using Sm = PrepSmem<DP>;
     constexpr int CH = DP / 8, NI = Sm::NI, NP = Sm::NP, kTri = Sm::kTri;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float g_hi[kChunk], g_lo[kChunk], s_beta[kChunk];
@@ -56,9 +56,9 @@ delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     const uint32_t sK = base, sQ = base + Sm::kQ, sN = base + Sm::kN;
     float* diag = reinterpret_cast<float*>(smem + Sm::kDiag);
 
-    load_rows<F32, DP>(sK, in.k, row3(in.k_stride).at(b, hk, 0), in.k_stride[2], t0, len, in.D,
+    load_rows_split<DP>(sK, in.k, row3(in.k_stride).at(b, hk, 0), in.k_stride[2], t0, len, in.D,
                        tid, 128);
-    load_rows<F32, DP>(sQ, in.q, row3(in.q_stride).at(b, hk, 0), in.q_stride[2], t0, len, in.D,
+    load_rows_split<DP>(sQ, in.q, row3(in.q_stride).at(b, hk, 0), in.q_stride[2], t0, len, in.D,
                        tid, 128);
     cp_commit();
 
@@ -68,7 +68,7 @@ delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     cp_wait<0>();
     __syncthreads();
 
-    if (F32 && h % ratio == 0) {      // the planes of k and q that the chains load
+    if (h % ratio == 0) {      // the planes of k and q that the chains load
         unsigned char* out = ws.planes(b * in.Hk + hk, chunk);
         for (int i = tid; i < 2 * Sm::kQ / 16; i += 128)
             reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(smem)[i];
@@ -261,37 +261,36 @@ delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
 // holds DP / KS of them): their partial sums of Kh S and Qh S meet in shared
 // memory, the middle part is computed by each, the outputs are split between
 // them by token.
-template <bool F32, int DP, int KS, int SL, int STAGES, bool STATES>
+template <int DP, int KS, int SL, int STAGES, bool STATES>
 struct ChainSmem {
     static constexpr int kTile = kChunk * DP * 2;                 // a plane of K or Q
-    static constexpr int kPlanes = Planes<F32>::kInput, kSplit = Planes<F32>::kSplit;
     static constexpr int kLP = kChunk * kChunk * 2;               // a plane of L or P
-    static constexpr int kV = ValueTile<F32, SL>::kBytes;
+    static constexpr int kV = ValueTile<SL>::kBytes;
     static constexpr int kGates = 3 * kChunk * 4;
     // offsets in a stage
-    static constexpr int oK = 0, oL = oK + kPlanes * kTile, oV = oL + kSplit * kLP,
+    static constexpr int oK = 0, oL = oK + kPlanes * kTile, oV = oL + kPlanes * kLP,
                          oGates = oV + kV, oQ = oGates + kGates,
                          oP = oQ + (STATES ? 0 : kPlanes * kTile),
-                         kStage = oP + (STATES ? 0 : kSplit * kLP);
+                         kStage = oP + (STATES ? 0 : kPlanes * kLP);
     static constexpr int oExchange = STAGES * kStage;
     // per warp: partial sums, 8 tiles of 512 bytes (twice with outputs)
     static constexpr int kExchange = KS > 1 ? KS * SL * 8 * 512 * (STATES ? 1 : 2) : 0;
     static constexpr int oOut = oExchange + kExchange;
-    static constexpr int kOut = KS * SL * (STATES ? kChunk * 32 : (kChunk / KS) * 32);
+    static constexpr int kOut = STATES ? KS * SL * kChunk * 32 : 0;
     static constexpr int kBytes = oOut + kOut;
 };
 
 // STATES: instead of outputs, the starting state of every chunk and the final
 // one (as split S^T images) and Z (split) are written, for the backward pass.
-template <bool F32, int DP, int KS, int SL, int STAGES, bool STATES>
+template <int DP, int KS, int SL, int STAGES, bool STATES>
 __global__ void __launch_bounds__(32 * KS * SL)
 delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) {
-    using Sm = ChainSmem<F32, DP, KS, SL, STAGES, STATES>;
+    using Sm = ChainSmem<DP, KS, SL, STAGES, STATES>;
     constexpr int THREADS = 32 * KS * SL;
     constexpr int CH = DP / 8;            // 16-byte pieces of a K row
     constexpr int DK = DP / KS;           // key rows of a warp
     constexpr int NT = DK / 8;            // tiles of S^T in a warp
-    constexpr int NP = Planes<F32>::kSplit, NI = Planes<F32>::kInput;
+    constexpr int NP = kPlanes, NI = kPlanes;
     extern __shared__ __align__(128) unsigned char smem[];
     const uint32_t base = smem_u32(smem);
 
@@ -322,19 +321,11 @@ delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) 
     auto load = [&](int c, int stage) {
         const uint32_t st = base + stage * Sm::kStage;
         const int t0 = c * kChunk;
-        if constexpr (F32) {
-            const unsigned char* planes = ws.planes(b * in.Hk + hk, c);
-            copy_bytes(st + Sm::oK, planes, NI * Sm::kTile, tid, THREADS);
-            if constexpr (!STATES)
-                copy_bytes(st + Sm::oQ, planes + NI * Sm::kTile, NI * Sm::kTile, tid, THREADS);
-        } else {
-            load_rows<false, DP>(st + Sm::oK, in.k, row3(in.k_stride).at(b, hk, 0),
-                                 in.k_stride[2], t0, len, D, tid, THREADS);
-            if constexpr (!STATES)
-                load_rows<false, DP>(st + Sm::oQ, in.q, row3(in.q_stride).at(b, hk, 0),
-                                     in.q_stride[2], t0, len, D, tid, THREADS);
-        }
-        load_values<F32, SL>(st + Sm::oV, in.v, row3(in.v_stride).at(b, h, 0), in.v_stride[2], vb,
+        const unsigned char* planes = ws.planes(b * in.Hk + hk, c);
+        copy_bytes(st + Sm::oK, planes, NI * Sm::kTile, tid, THREADS);
+        if constexpr (!STATES)
+            copy_bytes(st + Sm::oQ, planes + NI * Sm::kTile, NI * Sm::kTile, tid, THREADS);
+        load_values<SL>(st + Sm::oV, in.v, row3(in.v_stride).at(b, h, 0), in.v_stride[2], vb,
                              t0, len, D, tid, THREADS);
         copy_bytes(st + Sm::oL, ws.L(head, c), NP * Sm::kLP, tid, THREADS);
         if constexpr (!STATES) copy_bytes(st + Sm::oP, ws.P(head, c), NP * Sm::kLP, tid, THREADS);
@@ -415,8 +406,7 @@ delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) 
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
             float V[2][4];
-            load_v<F32, SL>(V, smem + stage * Sm::kStage + Sm::oV, st + Sm::oV,
-                            np * 16, slice, lane);
+            load_v<SL>(V, smem + stage * Sm::kStage + Sm::oV, np * 16, slice, lane);
             float X[2][4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -512,9 +502,7 @@ delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) 
                 }
             }
             if (live)
-                store_out<F32, KS>(o, os.at(b, h, c * kChunk), os.t, O,
-                                   smem + Sm::oOut + warp * (kChunk / KS) * 32, part, v0,
-                                   len - c * kChunk, lane);
+                store_out<KS>(o, os.at(b, h, c * kChunk), os.t, O, part, v0, len - c * kChunk, lane);
         }
     }
     if constexpr (STATES) {
@@ -532,25 +520,25 @@ delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) 
     }
 }
 
-template <bool F32, int DP>
+template <int DP>
 cudaError_t prep(const la_delta& in, const DeltaWs& ws, cudaStream_t st) {
-    using Sm = PrepSmem<F32, DP>;
+    using Sm = PrepSmem<DP>;
     const int chunks = (in.T + kChunk - 1) / kChunk;
-    auto* kernel = delta_prep_kernel<F32, DP>;
+    auto* kernel = delta_prep_kernel<DP>;
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), Sm::kBytes);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)(in.B * in.Hv) * (unsigned)chunks, 128, Sm::kBytes, st>>>(in, ws, chunks);
     return cudaGetLastError();
 }
 
-template <bool F32, int DP, int KS, int SL, bool STATES>
+template <int DP, int KS, int SL, bool STATES>
 cudaError_t chain(const la_delta& in, const DeltaWs& ws, void* o, Row3 os, float* state_out,
                   cudaStream_t st) {
     // two stages where they fit (float32 planes of a 128-row state do not)
-    constexpr int STAGES = ChainSmem<F32, DP, KS, SL, 2, STATES>::kBytes <= 227 * 1024 ? 2 : 1;
-    using Sm = ChainSmem<F32, DP, KS, SL, STAGES, STATES>;
+    constexpr int STAGES = ChainSmem<DP, KS, SL, 2, STATES>::kBytes <= 227 * 1024 ? 2 : 1;
+    using Sm = ChainSmem<DP, KS, SL, STAGES, STATES>;
     static_assert(Sm::kBytes <= 227 * 1024, "shared memory of a block");
-    auto* kernel = delta_chain_kernel<F32, DP, KS, SL, STAGES, STATES>;
+    auto* kernel = delta_chain_kernel<DP, KS, SL, STAGES, STATES>;
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), Sm::kBytes);
     if (e != cudaSuccess) return e;
     const dim3 grid(in.B * in.Hv, (in.D + 16 * SL - 1) / (16 * SL));
@@ -558,20 +546,19 @@ cudaError_t chain(const la_delta& in, const DeltaWs& ws, void* o, Row3 os, float
     return cudaGetLastError();
 }
 
-template <bool F32, int DP>
+// A slice of 16 value columns a block (two, which share the chunk's tiles: 368 us
+// beside 295 for 40 heads of 112 with 1000 tokens).
+template <int DP>
 cudaError_t forward(const la_delta& in, const DeltaWs& ws, void* o, Row3 os, float* state_out,
                     cudaStream_t st) {
-    cudaError_t e = F32 ? prep<true, DP>(in, ws, st) : launch_delta_tc_prep(in, ws, false, st);
-    if (e != cudaSuccess) return e;
-    if constexpr (F32) return chain<F32, DP, 4, 1, false>(in, ws, o, os, state_out, st);
-    else return launch_delta_tc_chain(in, ws, o, os, state_out, false, st);
+    const cudaError_t e = prep<DP>(in, ws, st);
+    return e != cudaSuccess ? e : chain<DP, 4, 1, false>(in, ws, o, os, state_out, st);
 }
 
-template <bool F32, int DP>
+template <int DP>
 cudaError_t states(const la_delta& in, const DeltaWs& ws, cudaStream_t st) {
-    cudaError_t e = prep<F32, DP>(in, ws, st);
-    if (e != cudaSuccess) return e;
-    return chain<F32, DP, 4, 1, true>(in, ws, nullptr, Row3{0, 0, 0}, nullptr, st);
+    const cudaError_t e = prep<DP>(in, ws, st);
+    return e != cudaSuccess ? e : chain<DP, 4, 1, true>(in, ws, nullptr, Row3{0, 0, 0}, nullptr, st);
 }
 
 }  // namespace
@@ -599,17 +586,16 @@ cudaError_t launch_delta_chunked(const la_delta& in, void* o, const long long o_
                                  float* state_out, void* ws_mem, cudaStream_t st) {
     const DeltaWs ws = DeltaWs::layout(ws_mem, 0, in.dt, in.B, in.Hk, in.Hv, in.T, in.D);
     const Row3 os = row3(o_stride);
-    if (in.dt == LA_BF16)
-        return in.D <= 64 ? forward<false, 64>(in, ws, o, os, state_out, st)
-                          : forward<false, 128>(in, ws, o, os, state_out, st);
-    return in.D <= 64 ? forward<true, 64>(in, ws, o, os, state_out, st)
-                      : forward<true, 128>(in, ws, o, os, state_out, st);
+    if (in.dt == LA_BF16) {
+        const cudaError_t e = launch_delta_tc_prep(in, ws, false, st);
+        return e != cudaSuccess ? e : launch_delta_tc_chain(in, ws, o, os, state_out, false, st);
+    }
+    return in.D <= 64 ? forward<64>(in, ws, o, os, state_out, st)
+                      : forward<128>(in, ws, o, os, state_out, st);
 }
 
 cudaError_t launch_delta_states(const la_delta& in, const DeltaWs& ws, cudaStream_t st) {
-    if (in.dt == LA_BF16)
-        return in.D <= 64 ? states<false, 64>(in, ws, st) : states<false, 128>(in, ws, st);
-    return in.D <= 64 ? states<true, 64>(in, ws, st) : states<true, 128>(in, ws, st);
+    return in.D <= 64 ? states<64>(in, ws, st) : states<128>(in, ws, st);
 }
 
 }  // namespace la

@@ -1,4 +1,5 @@
-// Backward pass of the gated delta rule in chunks of 64 tokens.
+// Backward pass of the gated delta rule in chunks of 64 tokens: the formulas, and
+// the kernels for float32 inputs (bf16: delta_tc_reverse.cu, delta_tc_grad.cu).
 //
 // With the forward pass's notation (delta_chunk.cu), dS the gradient of the
 // state after a chunk and dO that of its outputs:
@@ -6,7 +7,7 @@
 //     dS0 = gamma_63 dS + Qh^T (gamma o dO) - Kh^T (gamma B dX).
 // delta_reverse_kernel walks a head's chunks from the last to the first with
 // these and leaves dS and dX of every chunk.  delta_grad_kernel then forms, for
-// all chunks at once,
+// all chunks at once, from S0, Z, dS and dX,
 //     dV = B dX,   dbeta_i = dX_i . Z_i,   dP_ij = dO_i . U_j (i >= j),
 //     dQh = gamma o (dO S0^T) + (dP o E) Kh,
 //     dKh = -gamma B dX S0^T + (e^{G_63 - G} o U) dS^T + (dP o E)^T Qh + (N' + N'^T) Kh,
@@ -14,8 +15,6 @@
 //     dG_i = qh_i . dQh_i - v_i . dV_i,  and + <dS, S> (S after the chunk) at its last token,
 // where dG_i follows from the invariance of the chunk's outputs under a scaling
 // of what token i sees; dlog_alpha is dG summed from the chunk's end.
-#include <type_traits>
-
 #include "delta_tiles.cuh"
 
 namespace la {
@@ -27,15 +26,14 @@ namespace {
 // The columns of dS evolve independently as those of S do, and the kernel is
 // the forward chain's mirror: a warp holds dS^T of 16 value columns and DP / KS
 // key rows; dO takes v's place.
-template <bool F32, int DP, int KS, int SL, int STAGES>
+template <int DP, int KS, int SL, int STAGES>
 struct ReverseSmem {
     static constexpr int kTile = kChunk * DP * 2;
-    static constexpr int kPlanes = Planes<F32>::kInput, kSplit = Planes<F32>::kSplit;
     static constexpr int kLP = kChunk * kChunk * 2;
-    static constexpr int kV = ValueTile<F32, SL>::kBytes;
+    static constexpr int kV = ValueTile<SL>::kBytes;
     static constexpr int kGates = 3 * kChunk * 4;
     static constexpr int oK = 0, oQ = oK + kPlanes * kTile, oL = oQ + kPlanes * kTile,
-                         oP = oL + kSplit * kLP, oV = oP + kSplit * kLP, oGates = oV + kV,
+                         oP = oL + kPlanes * kLP, oV = oP + kPlanes * kLP, oGates = oV + kV,
                          kStage = oGates + kGates;
     static constexpr int oExchange = STAGES * kStage;
     static constexpr int kExchange = KS * SL * 8 * 512;
@@ -43,13 +41,13 @@ struct ReverseSmem {
     static constexpr int kBytes = oOut + SL * kChunk * 32;
 };
 
-template <bool F32, int DP, int KS, int SL, int STAGES>
+template <int DP, int KS, int SL, int STAGES>
 __global__ void __launch_bounds__(32 * KS * SL)
 delta_reverse_kernel(la_delta in, DeltaGrad grad, DeltaWs ws) {
-    using Sm = ReverseSmem<F32, DP, KS, SL, STAGES>;
+    using Sm = ReverseSmem<DP, KS, SL, STAGES>;
     constexpr int THREADS = 32 * KS * SL;
     constexpr int CH = DP / 8, DK = DP / KS, NT = DK / 8;
-    constexpr int NP = Planes<F32>::kSplit, NI = Planes<F32>::kInput;
+    constexpr int NP = kPlanes, NI = kPlanes;
     extern __shared__ __align__(128) unsigned char smem[];
     const uint32_t base = smem_u32(smem);
 
@@ -79,15 +77,9 @@ delta_reverse_kernel(la_delta in, DeltaGrad grad, DeltaWs ws) {
     auto load = [&](int c, int stage) {
         const uint32_t st = base + stage * Sm::kStage;
         const int t0 = c * kChunk;
-        if constexpr (F32) {              // the planes of K, then of Q
-            copy_bytes(st + Sm::oK, ws.planes(b * in.Hk + hk, c), 2 * NI * Sm::kTile, tid, THREADS);
-        } else {
-            load_rows<false, DP>(st + Sm::oK, in.k, row3(in.k_stride).at(b, hk, 0),
-                                 in.k_stride[2], t0, len, D, tid, THREADS);
-            load_rows<false, DP>(st + Sm::oQ, in.q, row3(in.q_stride).at(b, hk, 0),
-                                 in.q_stride[2], t0, len, D, tid, THREADS);
-        }
-        load_values<F32, SL>(st + Sm::oV, grad.d_o, row3(grad.do_stride).at(b, h, 0),
+        // the planes of K, then of Q
+        copy_bytes(st + Sm::oK, ws.planes(b * in.Hk + hk, c), 2 * NI * Sm::kTile, tid, THREADS);
+        load_values<SL>(st + Sm::oV, grad.d_o, row3(grad.do_stride).at(b, h, 0),
                              grad.do_stride[2], vb, t0, len, D, tid, THREADS);
         copy_bytes(st + Sm::oL, ws.L(head, c), NP * Sm::kLP, tid, THREADS);
         copy_bytes(st + Sm::oP, ws.P(head, c), NP * Sm::kLP, tid, THREADS);
@@ -143,7 +135,7 @@ delta_reverse_kernel(la_delta in, DeltaGrad grad, DeltaWs ws) {
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
             float V[2][4], W[2][4];
-            load_v<F32, SL>(V, smem + stage * Sm::kStage + Sm::oV, st + Sm::oV, np * 16, slice, lane);
+            load_v<SL>(V, smem + stage * Sm::kStage + Sm::oV, np * 16, slice, lane);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float2 ga =
@@ -254,10 +246,10 @@ delta_reverse_kernel(la_delta in, DeltaGrad grad, DeltaWs ws) {
 // share it, in their order.  Warp w: 16 tokens (w % 4) and half of the columns.
 constexpr int kGradThreads = 256;
 
-template <bool F32, int DP>
+template <int DP>
 struct GradSmem {
     static constexpr int kTile = kChunk * DP * 2;
-    static constexpr int NI = Planes<F32>::kInput, NP = Planes<F32>::kSplit;
+    static constexpr int NI = kPlanes, NP = kPlanes;
     static constexpr int kTri = kChunk * kChunk * 2;
     // half of the rows of a state image; dO, then dP o E and N' + N'^T; Z, then K; dX, then Q
     static constexpr int o0 = 0, o1 = o0 + NP * kTile,
@@ -283,20 +275,9 @@ __device__ __forceinline__ void put8(float* p, const float (&x)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
-__device__ __forceinline__ void put8(__nv_bfloat16* p, const float (&x)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                              pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-}
 __device__ __forceinline__ float2 fetch2(const float* p) { return *reinterpret_cast<const float2*>(p); }
-__device__ __forceinline__ float2 fetch2(const __nv_bfloat16* p) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
 __device__ __forceinline__ void put2(float* p, float x, float y) {
     *reinterpret_cast<float2*>(p) = make_float2(x, y);
-}
-__device__ __forceinline__ void put2(__nv_bfloat16* p, float x, float y) {
-    *reinterpret_cast<uint32_t*>(p) = pack_bf16(x, y);
 }
 
 // Eight values from planes `plane` elements apart.
@@ -325,11 +306,11 @@ __device__ __forceinline__ void load_planes(uint32_t dst, const __nv_bfloat16* s
     }
 }
 
-template <bool F32, int DP>
+template <int DP>
 __global__ void __launch_bounds__(kGradThreads)
 delta_grad_kernel(la_delta in, DeltaGrad grad, DeltaWs ws, int chunks) {
-    using Sm = GradSmem<F32, DP>;
-    using T = std::conditional_t<F32, float, __nv_bfloat16>;
+    using Sm = GradSmem<DP>;
+    using T = float;
     constexpr int CH = DP / 8, NP = Sm::NP, NI = Sm::NI, kTile = Sm::kTile, kTri = Sm::kTri;
     constexpr int NT = DP / 16;                 // tiles of a warp's columns
     extern __shared__ __align__(128) unsigned char smem[];
@@ -384,7 +365,7 @@ delta_grad_kernel(la_delta in, DeltaGrad grad, DeltaWs ws, int chunks) {
         __syncthreads();                        // the last head's readers are done
         for (int i = tid; i < kGateRows * kChunk; i += kGradThreads)
             (&gates[0][0])[i] = ws.gates(head, chunk)[i];
-        load_rows<F32, DP>(r1, grad.d_o, row3(grad.do_stride).at(b, h, 0), grad.do_stride[2], t0,
+        load_rows_split<DP>(r1, grad.d_o, row3(grad.do_stride).at(b, h, 0), grad.do_stride[2], t0,
                            len, D, tid, kGradThreads);
         load_planes<NP, DP>(r2, ws.Z(head, chunk), (size_t)kChunk * DP, kChunk, tid);
         load_planes<NP, DP>(r3, ws.dX(head, chunk), (size_t)kChunk * DP, kChunk, tid);
@@ -562,9 +543,9 @@ delta_grad_kernel(la_delta in, DeltaGrad grad, DeltaWs ws, int chunks) {
                 }
             }
         }
-        load_rows<F32, DP>(r2, in.k, row3(in.k_stride).at(b, hk, 0), in.k_stride[2], t0, len, D,
+        load_rows_split<DP>(r2, in.k, row3(in.k_stride).at(b, hk, 0), in.k_stride[2], t0, len, D,
                            tid, kGradThreads);
-        load_rows<F32, DP>(r3, in.q, row3(in.q_stride).at(b, hk, 0), in.q_stride[2], t0, len, D,
+        load_rows_split<DP>(r3, in.q, row3(in.q_stride).at(b, hk, 0), in.q_stride[2], t0, len, D,
                            tid, kGradThreads);
         cp_commit();
         cp_wait<0>();
@@ -689,27 +670,33 @@ delta_grad_kernel(la_delta in, DeltaGrad grad, DeltaWs ws, int chunks) {
     }
 }
 
-template <bool F32, int DP>
-cudaError_t backward(const la_delta& in, const DeltaGrad& g, const DeltaWs& ws, cudaStream_t st) {
+template <int DP>
+cudaError_t reverse(const la_delta& in, const DeltaGrad& g, const DeltaWs& ws, cudaStream_t st) {
     constexpr int KS = 4, SL = 1;
-    constexpr int STAGES = ReverseSmem<F32, DP, KS, SL, 2>::kBytes <= 227 * 1024 ? 2 : 1;
-    using Rs = ReverseSmem<F32, DP, KS, SL, STAGES>;
-    using Gs = GradSmem<F32, DP>;
-    static_assert(Rs::kBytes <= 227 * 1024 && Gs::kBytes <= 220 * 1024, "shared memory of a block");
-    const int chunks = (in.T + kChunk - 1) / kChunk;
-    cudaError_t e;
-    if (chunks > 0 && (e = launch_delta_states(in, ws, st)) != cudaSuccess) return e;
-    auto* reverse = delta_reverse_kernel<F32, DP, KS, SL, STAGES>;
-    if ((e = ensure_dyn_smem(reinterpret_cast<const void*>(reverse), Rs::kBytes)) != cudaSuccess)
-        return e;
+    constexpr int STAGES = ReverseSmem<DP, KS, SL, 2>::kBytes <= 227 * 1024 ? 2 : 1;
+    using Rs = ReverseSmem<DP, KS, SL, STAGES>;
+    static_assert(Rs::kBytes <= 227 * 1024, "shared memory of a block");
+    auto* kernel = delta_reverse_kernel<DP, KS, SL, STAGES>;
+    const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), Rs::kBytes);
+    if (e != cudaSuccess) return e;
     const dim3 grid(in.B * in.Hv, (in.D + 16 * SL - 1) / (16 * SL));
-    reverse<<<grid, 32 * KS * SL, Rs::kBytes, st>>>(in, g, ws);
-    if ((e = cudaGetLastError()) != cudaSuccess || chunks == 0) return e;
-    auto* grads = delta_grad_kernel<F32, DP>;
+    kernel<<<grid, 32 * KS * SL, Rs::kBytes, st>>>(in, g, ws);
+    return cudaGetLastError();
+}
+
+template <int DP>
+cudaError_t backward(const la_delta& in, const DeltaGrad& g, const DeltaWs& ws, cudaStream_t st) {
+    using Gs = GradSmem<DP>;
+    static_assert(Gs::kBytes <= 220 * 1024, "shared memory of a block");
+    cudaError_t e = cudaSuccess;
+    if (ws.chunks > 0 && (e = launch_delta_states(in, ws, st)) != cudaSuccess) return e;
+    e = reverse<DP>(in, g, ws, st);
+    if (e != cudaSuccess || ws.chunks == 0) return e;
+    auto* grads = delta_grad_kernel<DP>;
     if ((e = ensure_dyn_smem(reinterpret_cast<const void*>(grads), Gs::kBytes)) != cudaSuccess)
         return e;
-    grads<<<(unsigned)(in.B * in.Hk) * (unsigned)chunks, kGradThreads, Gs::kBytes, st>>>(in, g, ws,
-                                                                                         chunks);
+    grads<<<(unsigned)(in.B * in.Hk) * (unsigned)ws.chunks, kGradThreads, Gs::kBytes, st>>>(
+        in, g, ws, ws.chunks);
     return cudaGetLastError();
 }
 
@@ -718,8 +705,9 @@ cudaError_t backward(const la_delta& in, const DeltaGrad& g, const DeltaWs& ws, 
 cudaError_t launch_delta_backward(const la_delta& in, const DeltaGrad& g, void* ws_mem,
                                   cudaStream_t st) {
     const DeltaWs ws = DeltaWs::layout(ws_mem, 1, in.dt, in.B, in.Hk, in.Hv, in.T, in.D);
+    cudaError_t e = cudaSuccess;
+    if (in.T == 0 && (e = cudaMemsetAsync(ws.status, 0, 8, st)) != cudaSuccess) return e;
     if (in.dt == LA_BF16) {
-        cudaError_t e = cudaSuccess;
         if (in.T > 0) {
             if ((e = launch_delta_tc_prep(in, ws, true, st)) != cudaSuccess) return e;
             if ((e = launch_delta_tc_chain(in, ws, nullptr, Row3{0, 0, 0}, nullptr, true, st)) !=
@@ -729,7 +717,7 @@ cudaError_t launch_delta_backward(const la_delta& in, const DeltaGrad& g, void* 
         if ((e = launch_delta_tc_reverse(in, g, ws, st)) != cudaSuccess || in.T == 0) return e;
         return launch_delta_tc_grad(in, g, ws, st);
     }
-    return in.D <= 64 ? backward<true, 64>(in, g, ws, st) : backward<true, 128>(in, g, ws, st);
+    return in.D <= 64 ? backward<64>(in, g, ws, st) : backward<128>(in, g, ws, st);
 }
 
 }  // namespace la

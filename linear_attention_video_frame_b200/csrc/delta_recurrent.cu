@@ -11,7 +11,8 @@
 // One token is bound by the state's traffic (8 D^2 bytes a head).  A block of
 // 256 threads holds 16 KB of a 128-row state: 8 threads side by side take one
 // 128-byte row piece, so every access is a full line, and each thread has its
-// four 16-byte loads in flight at once.
+// four 16-byte loads in flight at once.  192 x 32 heads of 128: 151 us, 5.3 TB/s
+// (with k and q in registers and three blocks an SM 187 us).
 #include <cuda_bf16.h>
 
 #include "token.cuh"
@@ -35,7 +36,8 @@ __device__ __forceinline__ void st_out(__nv_bfloat16* p, float x) { *p = __float
 // ROWS: state rows of a thread (rows rg, rg + 32, ...).
 template <typename T, int ROWS>
 __global__ void __launch_bounds__(kThreads)
-delta_recurrent_kernel(la_delta in, T* o, Row3 os, float* state_out) {
+delta_recurrent_kernel(la_delta in, T* o, Row3 os, float* state_out, unsigned int* status) {
+    if (status && blockIdx.x + blockIdx.y + blockIdx.z == 0 && threadIdx.x < 2) status[threadIdx.x] = 0;
     // Per warp: partial k.S and q.S of the block's columns, and q.k; two
     // buffers so that one barrier a token is enough.
     __shared__ float4 part[2][kThreads / 32][kCols / 4][2];
@@ -144,7 +146,8 @@ delta_recurrent_kernel(la_delta in, T* o, Row3 os, float* state_out) {
 // values and five blocks (80 KB of loads) are in flight on an SM.
 template <typename T, int ROWS>
 __global__ void __launch_bounds__(kThreads, ROWS > 4 ? 3 : 5)
-delta_step_kernel(la_delta in, T* o, Row3 os, float* state_out) {
+delta_step_kernel(la_delta in, T* o, Row3 os, float* state_out, unsigned int* status) {
+    if (status && blockIdx.x + blockIdx.y + blockIdx.z == 0 && threadIdx.x < 2) status[threadIdx.x] = 0;
     __shared__ float4 part[kThreads / 32][kCols / 4][2];
     __shared__ float dots[kThreads / 32];
     __shared__ float2 kq[ROWS * kRowGroups];
@@ -248,33 +251,33 @@ delta_step_kernel(la_delta in, T* o, Row3 os, float* state_out) {
 
 template <typename T>
 void launch_typed(const la_delta& in, void* o, const long long os[3], float* state_out,
-                  cudaStream_t st) {
+                  unsigned int* status, cudaStream_t st) {
     const dim3 grid((in.D + kCols - 1) / kCols, in.Hv, in.B);
     T* out = static_cast<T*>(o);
     const Row3 r = o ? row3(os) : Row3{0, 0, 0};
     if (in.T == 1) {
         if (in.D <= 64)
-            delta_step_kernel<T, 2><<<grid, kThreads, 0, st>>>(in, out, r, state_out);
+            delta_step_kernel<T, 2><<<grid, kThreads, 0, st>>>(in, out, r, state_out, status);
         else if (in.D <= 128)
-            delta_step_kernel<T, 4><<<grid, kThreads, 0, st>>>(in, out, r, state_out);
+            delta_step_kernel<T, 4><<<grid, kThreads, 0, st>>>(in, out, r, state_out, status);
         else
-            delta_step_kernel<T, 8><<<grid, kThreads, 0, st>>>(in, out, r, state_out);
+            delta_step_kernel<T, 8><<<grid, kThreads, 0, st>>>(in, out, r, state_out, status);
         return;
     }
     if (in.D <= 64)
-        delta_recurrent_kernel<T, 2><<<grid, kThreads, 0, st>>>(in, out, r, state_out);
+        delta_recurrent_kernel<T, 2><<<grid, kThreads, 0, st>>>(in, out, r, state_out, status);
     else if (in.D <= 128)
-        delta_recurrent_kernel<T, 4><<<grid, kThreads, 0, st>>>(in, out, r, state_out);
+        delta_recurrent_kernel<T, 4><<<grid, kThreads, 0, st>>>(in, out, r, state_out, status);
     else
-        delta_recurrent_kernel<T, 8><<<grid, kThreads, 0, st>>>(in, out, r, state_out);
+        delta_recurrent_kernel<T, 8><<<grid, kThreads, 0, st>>>(in, out, r, state_out, status);
 }
 
 }  // namespace
 
 cudaError_t launch_delta_recurrent(const la_delta& in, void* o, const long long o_stride[3],
-                                   float* state_out, cudaStream_t st) {
-    if (in.dt == LA_BF16) launch_typed<__nv_bfloat16>(in, o, o_stride, state_out, st);
-    else launch_typed<float>(in, o, o_stride, state_out, st);
+                                   float* state_out, unsigned int* status, cudaStream_t st) {
+    if (in.dt == LA_BF16) launch_typed<__nv_bfloat16>(in, o, o_stride, state_out, status, st);
+    else launch_typed<float>(in, o, o_stride, state_out, status, st);
     return cudaGetLastError();
 }
 

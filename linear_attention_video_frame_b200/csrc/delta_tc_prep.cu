@@ -74,9 +74,9 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     float* diag = reinterpret_cast<float*>(smem + Sm::oDiag + warp * Sm::kDiag);
     const int g = lane >> 2, tq = lane & 3;
 
-    load_rows<false, DP>(sK, in.k, row3(in.k_stride).at(b, hk, 0), in.k_stride[2], t0, len, in.D,
+    load_rows<DP>(sK, in.k, row3(in.k_stride).at(b, hk, 0), in.k_stride[2], t0, len, in.D,
                          tid, 128);
-    load_rows<false, DP>(sQ, in.q, row3(in.q_stride).at(b, hk, 0), in.q_stride[2], t0, len, in.D,
+    load_rows<DP>(sQ, in.q, row3(in.q_stride).at(b, hk, 0), in.q_stride[2], t0, len, in.D,
                          tid, 128);
     cp_commit();
     if (warp == 3)

@@ -6,14 +6,11 @@
 
 namespace la {
 
-// Planes that a computed operand is split into (float32 values as sums of
-// bf16, see mma.cuh), and planes of the inputs.  bf16 inputs are exact in one
-// plane.  Computed values take three (2^-27): states and gate gradients leave in
-// float32, where two planes would show (3e-6 of the state in place of 1e-7).
-template <bool F32> struct Planes {
-    static constexpr int kSplit = 3;
-    static constexpr int kInput = F32 ? 3 : 1;
-};
+// bf16 planes of a float32 value (mma.cuh).  Computed values take three (2^-27):
+// states and gate gradients leave in float32, where two planes would show (3e-6 of
+// the state in place of 1e-7).  bf16 inputs are exact in one, float32 ones take
+// three as well.
+constexpr int kPlanes = 3;
 
 // Per token: exp(G), exp(G_63 - G), beta, and G as the sum of two floats.
 constexpr int kGateRows = 5;
@@ -61,7 +58,7 @@ struct DeltaWs {
     unsigned int* status;        // header of the workspace (la_query_device_status)
     unsigned char *gates_, *L_, *P_, *Kt_, *planes_, *states_, *dstates_, *Z_, *dX_;
     int chunks;          // per head
-    int DP, D, NP;
+    int DP, D;
     size_t bytes;
     Segments seg;
     float *seg_state, *seg_A, *seg_B;    // [head][segment][D][D], as states
@@ -72,7 +69,6 @@ struct DeltaWs {
         w.chunks = (T + kChunk - 1) / kChunk;
         w.DP = D <= 64 ? 64 : 128;
         w.D = D;
-        w.NP = dt == LA_F32 ? Planes<true>::kSplit : Planes<false>::kSplit;
         const size_t n = (size_t)B * Hv * w.chunks, nk = (size_t)B * Hk * w.chunks;
         size_t at = kWsHeaderBytes;
         unsigned char* p = static_cast<unsigned char*>(mem);
@@ -83,10 +79,10 @@ struct DeltaWs {
             return r;
         };
         w.gates_ = take(n * kGateRows * kChunk * 4);
-        w.L_ = take(n * w.NP * 2 * kChunk * kChunk);
-        w.P_ = take(n * w.NP * 2 * kChunk * kChunk);
+        w.L_ = take(n * kPlanes * 2 * kChunk * kChunk);
+        w.P_ = take(n * kPlanes * 2 * kChunk * kChunk);
         w.Kt_ = take(dt == LA_BF16 ? n * 3 * w.plane_bytes() : 0);
-        w.planes_ = take(dt == LA_F32 ? nk * 2 * w.NP * w.plane_bytes() : 0);
+        w.planes_ = take(dt == LA_F32 ? nk * 2 * kPlanes * w.plane_bytes() : 0);
         w.seg = dt == LA_BF16 ? Segments::plan(backward, B * Hv, w.chunks) : Segments{1, w.chunks};
         if (w.seg.count > 1) {
             const size_t all = (size_t)B * Hv * w.seg.count * D * D * 4;
@@ -96,7 +92,7 @@ struct DeltaWs {
         }
         if (backward) {
             const size_t image = dt == LA_F32 ? w.image_bytes() : w.state_frag_bytes();
-            const size_t rows = dt == LA_F32 ? w.NP * w.plane_bytes() : kRowFragBytes;
+            const size_t rows = dt == LA_F32 ? kPlanes * w.plane_bytes() : kRowFragBytes;
             w.states_ = take((size_t)B * Hv * (w.chunks + 1) * image);
             w.dstates_ = take(n * image);
             if (dt == LA_BF16 && Hv > Hk) {
@@ -111,7 +107,7 @@ struct DeltaWs {
         return w;
     }
     __host__ __device__ size_t plane_bytes() const { return (size_t)kChunk * DP * 2; }
-    __host__ __device__ size_t image_bytes() const { return (size_t)D * DP * 2 * NP; }
+    __host__ __device__ size_t image_bytes() const { return (size_t)D * DP * 2 * kPlanes; }
     __device__ float* segment(float* base, int head, int s) const {
         return base + ((size_t)head * seg.count + s) * D * D;
     }
@@ -137,10 +133,10 @@ struct DeltaWs {
         return reinterpret_cast<float*>(gates_) + at(head, c) * kGateRows * kChunk;
     }
     __device__ __nv_bfloat16* L(int head, int c) const {
-        return reinterpret_cast<__nv_bfloat16*>(L_) + at(head, c) * NP * kChunk * kChunk;
+        return reinterpret_cast<__nv_bfloat16*>(L_) + at(head, c) * kPlanes * kChunk * kChunk;
     }
     __device__ __nv_bfloat16* P(int head, int c) const {
-        return reinterpret_cast<__nv_bfloat16*>(P_) + at(head, c) * NP * kChunk * kChunk;
+        return reinterpret_cast<__nv_bfloat16*>(P_) + at(head, c) * kPlanes * kChunk * kChunk;
     }
     // bf16 inputs: Kt as [half of 64 columns][plane][64 rows of 128 bytes], swizzled
     __device__ unsigned char* Kt(int head, int c) const {
@@ -148,7 +144,7 @@ struct DeltaWs {
     }
     // float32 inputs: the planes of K, then of Q, as shared-memory tiles
     __device__ unsigned char* planes(int khead, int c) const {
-        return planes_ + ((size_t)khead * chunks + c) * 2 * NP * plane_bytes();
+        return planes_ + ((size_t)khead * chunks + c) * 2 * kPlanes * plane_bytes();
     }
     __device__ __nv_bfloat16* states(int head, int c) const {       // c = 0 .. chunks
         return reinterpret_cast<__nv_bfloat16*>(
@@ -158,10 +154,10 @@ struct DeltaWs {
         return reinterpret_cast<__nv_bfloat16*>(dstates_ + at(head, c) * image_bytes());
     }
     __device__ __nv_bfloat16* Z(int head, int c) const {
-        return reinterpret_cast<__nv_bfloat16*>(Z_ + at(head, c) * NP * plane_bytes());
+        return reinterpret_cast<__nv_bfloat16*>(Z_ + at(head, c) * kPlanes * plane_bytes());
     }
     __device__ __nv_bfloat16* dX(int head, int c) const {
-        return reinterpret_cast<__nv_bfloat16*>(dX_ + at(head, c) * NP * plane_bytes());
+        return reinterpret_cast<__nv_bfloat16*>(dX_ + at(head, c) * kPlanes * plane_bytes());
     }
 };
 
@@ -185,39 +181,44 @@ cudaError_t launch_delta_states(const la_delta& in, const DeltaWs& ws, cudaStrea
 
 #ifdef __CUDACC__
 
-// Rows t0 .. t0 + 63 of a [T, D] matrix as bf16 tiles of DP columns: one plane
-// by asynchronous copies (bf16), or split planes (float32).  Rows from
-// `len` on and columns from D on are 0 and not read.
-template <bool F32, int DP>
+// Rows t0 .. t0 + 63 of a bf16 [T, D] matrix as a tile of DP columns, by
+// asynchronous copies.  Rows from `len` on and columns from D on are 0 and not read.
+template <int DP>
 __device__ __forceinline__ void load_rows(uint32_t dst, const void* src, long long offset,
                                           long long stride, int t0, int len, int D, int tid,
                                           int threads) {
     constexpr int CH = DP / 8;
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(src) + offset;
     for (int i = tid; i < kChunk * CH; i += threads) {
         const int r = i / CH, c = i % CH;
         const bool on = t0 + r < len && c * 8 < D;
-        const long long at = offset + (t0 + r) * stride + c * 8;
-        if constexpr (F32) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-            if (on) {
-                const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
-                x = p[0];
-                y = p[1];
-            }
-            constexpr int NP = Planes<true>::kInput;
-            const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            uint32_t w[4][NP];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) split_bf16<NP>(f[2 * e], f[2 * e + 1], w[e]);
-#pragma unroll
-            for (int j = 0; j < NP; ++j)
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};"
-                             :: "r"(dst + j * kChunk * DP * 2 + tile_at<CH>(r, c)), "r"(w[0][j]),
-                                "r"(w[1][j]), "r"(w[2][j]), "r"(w[3][j]) : "memory");
-        } else {
-            const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(src);
-            cp16(dst + tile_at<CH>(r, c), on ? p + at : p, on);
+        cp16(dst + tile_at<CH>(r, c), on ? p + (t0 + r) * stride + c * 8 : p, on);
+    }
+}
+// The same of a float32 matrix, split into planes.
+template <int DP>
+__device__ __forceinline__ void load_rows_split(uint32_t dst, const void* src, long long offset,
+                                                long long stride, int t0, int len, int D, int tid,
+                                                int threads) {
+    constexpr int CH = DP / 8;
+    for (int i = tid; i < kChunk * CH; i += threads) {
+        const int r = i / CH, c = i % CH;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (t0 + r < len && c * 8 < D) {
+            const float4* p = reinterpret_cast<const float4*>(
+                static_cast<const float*>(src) + offset + (t0 + r) * stride + c * 8);
+            x = p[0];
+            y = p[1];
         }
+        const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        uint32_t w[4][kPlanes];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_bf16<kPlanes>(f[2 * e], f[2 * e + 1], w[e]);
+#pragma unroll
+        for (int j = 0; j < kPlanes; ++j)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};"
+                         :: "r"(dst + j * kChunk * DP * 2 + tile_at<CH>(r, c)), "r"(w[0][j]),
+                            "r"(w[1][j]), "r"(w[2][j]), "r"(w[3][j]) : "memory");
     }
 }
 
@@ -333,53 +334,36 @@ __device__ __forceinline__ void sum_parts(float (&m)[4], const float4* ex, int n
     m[0] = s.x; m[1] = s.y; m[2] = s.z; m[3] = s.w;
 }
 
-// The block's value columns vb .. vb + 16 SL - 1 of a chunk's rows: bf16 as a
-// permuted tile, float32 as rows of SL * 16 + 4 floats.  0 where there is none.
-template <bool F32, int SL>
+// The block's value columns vb .. vb + 16 SL - 1 of a chunk's rows, as rows of
+// SL * 16 + 4 floats.  0 where there is none.
+template <int SL>
 struct ValueTile {
-    static constexpr int kPitch = F32 ? SL * 16 + 4 : SL * 16;   // elements
-    static constexpr int kBytes = kChunk * kPitch * (F32 ? 4 : 2);
+    static constexpr int kPitch = SL * 16 + 4;
+    static constexpr int kBytes = kChunk * kPitch * 4;
 };
-template <bool F32, int SL>
+template <int SL>
 __device__ __forceinline__ void load_values(uint32_t dst, const void* src, long long offset,
                                             long long stride, int vb, int t0, int len, int D,
                                             int tid, int threads) {
-    constexpr int N = F32 ? 4 : 8, CH = SL * 16 / N;
+    constexpr int CH = SL * 4;
     for (int i = tid; i < kChunk * CH; i += threads) {
         const int r = i / CH, c = i % CH;
-        const bool on = t0 + r < len && vb + c * N < D;
-        const long long at = on ? offset + (t0 + r) * stride + vb + c * N : 0;
-        if constexpr (F32)
-            cp16(dst + (r * ValueTile<true, SL>::kPitch + c * 4) * 4,
-                 static_cast<const float*>(src) + at, on);
-        else
-            cp16(dst + tile_at<SL * 2>(r, c), static_cast<const __nv_bfloat16*>(src) + at, on);
+        const bool on = t0 + r < len && vb + c * 4 < D;
+        cp16(dst + (r * ValueTile<SL>::kPitch + c * 4) * 4,
+             static_cast<const float*>(src) + (on ? offset + (t0 + r) * stride + vb + c * 4 : 0), on);
     }
 }
 
 // 16 tokens of a slice's 16 value columns, transposed into two product tiles.
-template <bool F32, int SL>
-__device__ __forceinline__ void load_v(float (&V)[2][4], const unsigned char* ptr, uint32_t addr,
-                                       int row, int slice, int lane) {
-    if constexpr (F32) {
-        constexpr int pitch = ValueTile<true, SL>::kPitch;
-        const float* v = reinterpret_cast<const float*>(ptr) + slice * 16 + (lane >> 2);
+template <int SL>
+__device__ __forceinline__ void load_v(float (&V)[2][4], const unsigned char* ptr, int row,
+                                       int slice, int lane) {
+    const float* v = reinterpret_cast<const float*>(ptr) + slice * 16 + (lane >> 2);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                V[j][e] = v[(row + j * 8 + 2 * (lane & 3) + (e & 1)) * pitch + 8 * (e >> 1)];
-    } else {
-        uint32_t r[4];      // (columns 0-7, tokens 0-7) (0-7, 8-15) (8-15, 0-7) (8-15, 8-15)
-        ldsm4_t(r, at_rows<SL * 2>(addr, row, slice * 2, lane));
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            V[j][0] = __uint_as_float(r[j] << 16);
-            V[j][1] = __uint_as_float(r[j] & 0xffff0000u);
-            V[j][2] = __uint_as_float(r[2 + j] << 16);
-            V[j][3] = __uint_as_float(r[2 + j] & 0xffff0000u);
-        }
-    }
+        for (int e = 0; e < 4; ++e)
+            V[j][e] = v[(row + j * 8 + 2 * (lane & 3) + (e & 1)) * ValueTile<SL>::kPitch + 8 * (e >> 1)];
 }
 
 // S^T tiles of a warp (16 value columns, key rows from k0) into an image.
@@ -430,40 +414,19 @@ __device__ __forceinline__ void store_rows(__nv_bfloat16* out, const float (&M)[
 }
 
 // A warp's share of the chunk's outputs: tokens 64 / KS * part .., `rows` of
-// the chunk's tokens exist.  `stage`: 64 / KS x 32 bytes of the warp's own.
-template <bool F32, int KS>
+// the chunk's tokens exist.
+template <int KS>
 __device__ __forceinline__ void store_out(void* o, long long offset, long long stride,
-                                          const float (&O)[8][4], unsigned char* stage, int part,
-                                          int v0, int rows, int lane) {
-    constexpr int TILES = 8 / KS;
-    if constexpr (F32) {
-        float* p = static_cast<float*>(o) + offset + v0 + (lane >> 2);
+                                          const float (&O)[8][4], int part, int v0, int rows,
+                                          int lane) {
+    float* p = static_cast<float*>(o) + offset + v0 + (lane >> 2);
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-            if (nt / TILES != part) continue;
+    for (int nt = 0; nt < 8; ++nt) {
+        if (nt / (8 / KS) != part) continue;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = nt * 8 + 2 * (lane & 3) + (e & 1);
-                if (t < rows) p[t * stride + 8 * (e >> 1)] = O[nt][e];
-            }
-        }
-    } else {
-        const uint32_t sm = smem_u32(stage);
-        __syncwarp();
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-            if (nt / TILES != part) continue;
-            stsm2_t(sm + ((nt % TILES) * 8 + (lane & 7)) * 32 + ((lane >> 3) & 1) * 16,
-                    pack_bf16(O[nt][0], O[nt][1]), pack_bf16(O[nt][2], O[nt][3]));
-        }
-        __syncwarp();
-        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(o) + offset + v0;
-#pragma unroll
-        for (int i = lane; i < TILES * 16; i += 32) {
-            const int t = part * TILES * 8 + (i >> 1);
-            if (t < rows)
-                *reinterpret_cast<uint4*>(p + t * stride + (i & 1) * 8) =
-                    *reinterpret_cast<const uint4*>(stage + i * 16);
+        for (int e = 0; e < 4; ++e) {
+            const int t = nt * 8 + 2 * (lane & 3) + (e & 1);
+            if (t < rows) p[t * stride + 8 * (e >> 1)] = O[nt][e];
         }
     }
 }

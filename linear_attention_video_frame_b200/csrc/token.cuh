@@ -35,8 +35,9 @@ __device__ __forceinline__ int seq_len(const int* lengths, int b, int T) {
 }
 
 // Launchers; each returns the CUDA error of its launches.
+// status: the words that la_query_device_status reads, or NULL.
 cudaError_t launch_delta_recurrent(const la_delta& in, void* o, const long long o_stride[3],
-                                   float* state_out, cudaStream_t st);
+                                   float* state_out, unsigned int* status, cudaStream_t st);
 // Chunked tensor-core path (delta_chunk.cu).
 bool delta_chunked(int backward, int T, int D);
 size_t delta_workspace_bytes(int backward, int dt, int B, int Hk, int Hv, int T, int D);

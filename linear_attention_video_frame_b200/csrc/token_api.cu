@@ -132,7 +132,8 @@ la_status forward(const la_delta* in, void* o, const long long os[3], float* sta
             if (overlaps(r.p, r.n, a.lengths, (size_t)a.B * 4)) return LA_ERR_INVALID_ARG;
     const cudaError_t e = !step && delta_chunked(0, a.T, a.D)
                               ? launch_delta_chunked(a, o, rs, state_out, ws, st)
-                              : launch_delta_recurrent(a, o, rs, state_out, st);
+                              : launch_delta_recurrent(a, o, rs, state_out,
+                                                       static_cast<unsigned int*>(ws), st);
     if (e != cudaSuccess) { cudaGetLastError(); return LA_ERR_CUDA; }
     return LA_OK;
 }
