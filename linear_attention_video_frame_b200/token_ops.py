@@ -121,12 +121,16 @@ def _full(t, name: str, shape, dtype, device):
     return t.data_ptr()
 
 
-def _space(workspace, need: int, device):
-    """A workspace's address (a new one's where None is given) and the tensor that owns it."""
+def _space(workspace, need: int, like: torch.Tensor, stream):
+    """The workspace of a call: the given one, or a new one.  A new one is let go when the call
+    returns, so the allocator has to know of another stream that its kernels run on."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif workspace.device != device:
-        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+        workspace = like.new_empty((need,), dtype=torch.uint8)
+        if stream is not None:
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                    else torch.cuda.ExternalStream(int(stream), like.device))
+    elif workspace.device != like.device:
+        raise ValueError(f"workspace is on {workspace.device}, expected {like.device}")
     return workspace
 
 
@@ -173,7 +177,9 @@ def _inputs(q, k, v, log_alpha, beta, k_scale, q_scale, state_in, lengths, devic
 
 def _new_rows(like: torch.Tensor, lengths) -> torch.Tensor:
     # rows behind a sequence's length are not written
-    return torch.empty_like(like) if lengths is None else torch.zeros_like(like)
+    o = torch.empty_like(like) if lengths is None else torch.zeros_like(like)
+    s = o.stride()
+    return o.contiguous() if s[-1] != 1 or 0 in s else o         # `like` was a broadcast view
 
 
 def la_gated_delta_rule(q, k, v, log_alpha, beta, k_scale: float = 1.0, q_scale: float = 1.0,
@@ -189,14 +195,12 @@ def la_gated_delta_rule(q, k, v, log_alpha, beta, k_scale: float = 1.0, q_scale:
     B, Hv, T, D = v.shape
     if o is None:
         o = _new_rows(v, lengths)
-        if o.stride(-1) != 1 or 0 in o.stride():         # v was a broadcast view
-            o = o.contiguous()
     os = _rows(o, "o", (B, Hv, T, D), q.dtype, device)
     end = _full(state_out, "state_out", (B, Hv, D, D), torch.float32, device)
     need = lib.la_delta_workspace_size(0, code, B, q.shape[1], Hv, T, D)
     if need == 0:
         raise LaScanError(LA_ERR_UNSUPPORTED, "la_gated_delta_rule")
-    workspace = _space(workspace, need, device)
+    workspace = _space(workspace, need, q, stream)
     st = lib.la_gated_delta_rule(a, o.data_ptr(), _pack_strides(*os), end, workspace.data_ptr(),
                                  workspace.numel(), _raw_stream(stream, device))
     if st != LA_OK:
@@ -220,8 +224,6 @@ def la_gated_delta_step(q, k, v, log_alpha, beta, state_in, k_scale: float = 1.0
     B, Hv, D = shape = v.shape
     if o is None:
         o = _new_rows(v, lengths)
-        if o.stride(-1) != 1 or 0 in o.stride():
-            o = o.contiguous()
     os = _rows(o, "o", shape, q.dtype, device)
     end = _full(state_out, "state_out", (B, Hv, D, D), torch.float32, device)
     st = lib.la_gated_delta_step(a, o.data_ptr(), _pack_strides(*os), end,
@@ -247,14 +249,14 @@ def la_gated_delta_rule_backward(q, k, v, log_alpha, beta, do, k_scale: float = 
     dos = _rows(do, "do", vshape, dtype, device)
 
     def out(t, shape, dt):
-        return torch.empty(shape, dtype=dt, device=device) if t is None else t
+        return q.new_empty(shape, dtype=dt) if t is None else t
 
     dq, dk, dv = out(dq, kshape, dtype), out(dk, kshape, dtype), out(dv, vshape, dtype)
     dlog_alpha, dbeta = out(dlog_alpha, vshape[:3], f32), out(dbeta, vshape[:3], f32)
     need = lib.la_delta_workspace_size(1, code, B, kshape[1], Hv, T, D)
     if need == 0:
         raise LaScanError(LA_ERR_UNSUPPORTED, "la_gated_delta_rule_backward")
-    workspace = _space(workspace, need, device)
+    workspace = _space(workspace, need, q, stream)
     st = lib.la_gated_delta_rule_backward(
         a, do.data_ptr(), _pack_strides(*dos),
         _full(dstate_out, "dstate_out", (B, Hv, D, D), f32, device),
@@ -282,18 +284,27 @@ def la_add_rms_norm_fp8(x, residual, weight, eps: float = 1e-6, group: int = 128
         raise ValueError(f"group must be 128 or 0 (the row), got {group}")
     device = _here(x, "x")
     groups = (*shape[:-1], -(-N // group) if group else 1)
-    if h is None and residual is not None:
+    px, pr = _full(x, "x", shape, dtype, device), _full(residual, "residual", shape, dtype, device)
+    pw = _full(weight, "weight", (N,), torch.float32, device)
+    if h is not None:
+        ph = _full(h, "h", shape, dtype, device)
+    elif residual is not None:
         h = torch.empty_like(x)
+        ph = h.data_ptr()
+    else:
+        ph = None
     if y is None:
-        y = torch.empty(shape, dtype=torch.float8_e4m3fn, device=device)
+        y = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+        py = y.data_ptr()
+    else:
+        py = _full(y, "y", shape, torch.float8_e4m3fn, device)
     if scale is None:
-        scale = torch.empty(groups, dtype=torch.float32, device=device)
-    st = lib.la_add_rms_norm_fp8(
-        _full(x, "x", shape, dtype, device), _full(residual, "residual", shape, dtype, device),
-        _full(weight, "weight", (N,), torch.float32, device), _full(h, "h", shape, dtype, device),
-        _full(y, "y", shape, torch.float8_e4m3fn, device),
-        _full(scale, "scale", groups, torch.float32, device), dt, x.numel() // N if N else 0, N,
-        group, eps, _raw_stream(stream, device))
+        scale = weight.new_empty(groups)
+        ps = scale.data_ptr()
+    else:
+        ps = _full(scale, "scale", groups, torch.float32, device)
+    st = lib.la_add_rms_norm_fp8(px, pr, pw, ph, py, ps, dt, x.numel() // N if N else 0, N, group,
+                                 eps, _raw_stream(stream, device))
     if st != LA_OK:
         _raise(st, "la_add_rms_norm_fp8")
     return y, scale, x if h is None else h
@@ -310,22 +321,25 @@ def la_add_rms_norm_backward(dy, h, weight, dh=None, eps: float = 1e-6, dx=None,
     dt = _dtype_code(h)
     device = _here(h, "h")
     rows = h.numel() // N if N else 0
+    ph, pdy = _full(h, "h", shape, dtype, device), _full(dy, "dy", shape, dtype, device)
+    pw, pdh = _full(weight, "weight", (N,), torch.float32, device), \
+        _full(dh, "dh", shape, dtype, device)
     if dx is None:
         dx = torch.empty_like(h)
-    space, size = None, 0
+        pdx = dx.data_ptr()
+    else:
+        pdx = _full(dx, "dx", shape, dtype, device)
+    pdw, space, size = None, None, 0
     if need_dweight:
         if dweight is None:
-            dweight = torch.empty((N,), dtype=torch.float32, device=device)
-        workspace = _space(workspace, lib.la_norm_workspace_size(rows, N), device)
+            dweight = torch.empty_like(weight)
+        pdw = _full(dweight, "dweight", (N,), torch.float32, device)
+        workspace = _space(workspace, lib.la_norm_workspace_size(rows, N), h, stream)
         space, size = workspace.data_ptr(), workspace.numel()
     else:
         dweight = None
-    st = lib.la_add_rms_norm_backward(
-        _full(dy, "dy", shape, dtype, device), _full(h, "h", shape, dtype, device),
-        _full(weight, "weight", (N,), torch.float32, device), _full(dh, "dh", shape, dtype, device),
-        _full(dx, "dx", shape, dtype, device),
-        _full(dweight, "dweight", (N,), torch.float32, device), dt, rows, N, eps, space, size,
-        _raw_stream(stream, device))
+    st = lib.la_add_rms_norm_backward(pdy, ph, pw, pdh, pdx, pdw, dt, rows, N, eps, space, size,
+                                      _raw_stream(stream, device))
     if st != LA_OK:
         _raise(st, "la_add_rms_norm_backward")
     return dx, dweight

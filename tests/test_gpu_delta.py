@@ -329,3 +329,25 @@ def test_long_sequence_offsets():
     o = big.as_strided((1, 1, T, D), (0, 0, stride, 1), 128)
     la.la_gated_delta_rule(*_args(x), state_in=x["state"], o=o, **_kw(x))
     assert _same(o, want[0])
+
+
+def test_other_stream_without_a_workspace():
+    """A call on a stream of its own keeps its own workspace until it has run, whatever the
+    current stream allocates and writes meanwhile."""
+    x = delta_inputs(1, 2, 2, 700, 128, seed=51)
+    want = _forward(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    B, Hv, T, D = x["v"].shape
+    end = torch.empty(B, Hv, D, D, device="cuda")
+    o = torch.empty_like(x["v"])
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200000)
+        la.la_gated_delta_rule(*_args(x), state_in=x["state"], state_out=end, o=o, **_kw(x),
+                               stream=side)
+        for _ in range(4):
+            torch.full((la.la_delta_workspace_size(False, la.LA_BF16, B, 2, Hv, T, D),), 255,
+                       dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert _same(o, want[0]) and _same(end, want[1])
