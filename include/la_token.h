@@ -9,9 +9,9 @@
  * 16-byte aligned, caller-owned buffers, work enqueued on `stream`, argument
  * errors returned before anything is enqueued, no allocation, no
  * synchronisation), except where a paragraph below says otherwise.  No call
- * here uses streams of the library's own, waits on the device, or uses
+ * here uses streams of the library's own, and no result depends on the order of
  * atomics: equal inputs give equal bits, and calls can be captured into CUDA
- * graphs.
+ * graphs.  Calls that may run at the same time need workspaces of their own.
  *
  * Gated delta rule, per batch item b and value head h, t = 1..T, the state S
  * key-major [D, D] as in la_scan.h:
@@ -69,8 +69,12 @@ typedef struct la_delta {
  * T == 0 writes the initial state to state_out and nothing else.
  * workspace: la_delta_workspace_size(0, ...) bytes, 256-byte aligned.
  *
- * 64 <= T and D <= 128 run chunked on tensor cores (chunks of 64 tokens);
- * shorter calls and wider heads run token by token in float32.
+ * Heads up to 128 wide run chunked on tensor cores (chunks of 64 tokens) from about
+ * 12 to 40 tokens on, by type and number of heads; shorter calls and wider heads run
+ * token by token in float32 (la_delta_plan tells).  With few heads a long sequence is
+ * cut into segments that run side by side.
+ * The chunked kernels bound every wait on the device; la_query_device_status(workspace,
+ * stream) tells whether one ran out (LA_ERR_TIMEOUT), as it does for the scans.
  */
 LA_API la_status la_gated_delta_rule(const la_delta* in, void* o, const long long o_stride[3],
                                      float* state_out, void* workspace, size_t workspace_bytes,

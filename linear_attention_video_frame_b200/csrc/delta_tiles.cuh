@@ -24,8 +24,8 @@ constexpr int kGateRows = 5;
 struct Segments {
     int count, chunks;           // of a head; of a segment
 
-    // Chunk times of the passes: rounds of jobs over the SMs (one job each), and
-    // what joining the segments costs (about 10 us, three chunk times).
+    // Chunk times (2 to 4 us) of the passes: rounds of jobs over the SMs, one job each;
+    // the second pass's start costs about three more, a join (10 to 23 us) six.
     static Segments plan(int backward, int heads, int chunks) {
         auto rounds = [](long long jobs) {
             return (double)((jobs + kDefaultSmCount - 1) / kDefaultSmCount);
@@ -39,7 +39,7 @@ struct Segments {
             const double forward = rounds((long long)heads * (s > 2 ? 2 * s - 3 : 1)) +
                                    rounds((long long)heads * (s - 1));
             const double reverse = backward ? 2.0 * rounds((long long)heads * (s - 1)) : 0.0;
-            const double cost = (forward + reverse) * each + 4.0 * passes;
+            const double cost = (forward + reverse) * each + (s > 2 ? 9.0 : 3.0) * passes;
             if (cost < 0.9 * least) {
                 least = cost;
                 best = Segments{s, each};

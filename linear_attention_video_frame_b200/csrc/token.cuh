@@ -39,7 +39,7 @@ __device__ __forceinline__ int seq_len(const int* lengths, int b, int T) {
 cudaError_t launch_delta_recurrent(const la_delta& in, void* o, const long long o_stride[3],
                                    float* state_out, unsigned int* status, cudaStream_t st);
 // Chunked tensor-core path (delta_chunk.cu).
-bool delta_chunked(int backward, int T, int D);
+bool delta_chunked(int backward, int dt, int heads, int T, int D);
 size_t delta_workspace_bytes(int backward, int dt, int B, int Hk, int Hv, int T, int D);
 int delta_kernel_count(int backward, int dt, int B, int Hk, int Hv, int T);
 cudaError_t launch_delta_chunked(const la_delta& in, void* o, const long long o_stride[3],

@@ -130,7 +130,7 @@ la_status forward(const la_delta* in, void* o, const long long os[3], float* sta
     if (a.lengths)
         for (const Region& r : outs)
             if (overlaps(r.p, r.n, a.lengths, (size_t)a.B * 4)) return LA_ERR_INVALID_ARG;
-    const cudaError_t e = !step && delta_chunked(0, a.T, a.D)
+    const cudaError_t e = !step && delta_chunked(0, a.dt, a.B * a.Hv, a.T, a.D)
                               ? launch_delta_chunked(a, o, rs, state_out, ws, st)
                               : launch_delta_recurrent(a, o, rs, state_out,
                                                        static_cast<unsigned int*>(ws), st);
@@ -166,7 +166,7 @@ extern "C" size_t la_delta_workspace_size(int backward, la_dtype dt, int B, int 
 extern "C" const char* la_delta_plan(int backward, la_dtype dt, int B, int Hk, int Hv, int T,
                                      int D, int* kernels) {
     if (la_delta_workspace_size(backward, dt, B, Hk, Hv, T, D) == 0) return nullptr;
-    const bool chunked = delta_chunked(backward, T, D);
+    const bool chunked = delta_chunked(backward, dt, B * Hv, T, D);
     if (kernels) *kernels = chunked ? delta_kernel_count(backward, dt, B, Hk, Hv, T) : 1;
     return chunked ? "delta_chunked" : "delta_recurrent";
 }

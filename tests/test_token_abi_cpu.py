@@ -90,8 +90,9 @@ def test_step_and_backward_refusals():
 
 
 def test_delta_sizes_and_plans():
-    assert la.la_delta_plan(False, la.LA_BF16, 1, 1, 1, 63, 64)[0] == "delta_recurrent"
-    assert la.la_delta_plan(False, la.LA_BF16, 1, 1, 1, 64, 64)[0] != "delta_recurrent"
+    for dt, heads, first in ((la.LA_BF16, 1, 24), (la.LA_BF16, 64, 12), (la.LA_F32, 64, 40)):
+        assert la.la_delta_plan(False, dt, 1, 1, heads, first - 1, 64) == ("delta_recurrent", 1)
+        assert la.la_delta_plan(False, dt, 1, 1, heads, first, 64) == ("delta_chunked", 2)
     assert la.la_delta_plan(False, la.LA_F32, 1, 1, 1, 64, 144)[0] == "delta_recurrent"
     assert la.la_delta_plan(True, la.LA_BF16, 1, 1, 1, 1, 64)[0] != "delta_recurrent"
     assert la.la_delta_plan(True, la.LA_BF16, 1, 1, 1, 1, 144) == (None, 0)
