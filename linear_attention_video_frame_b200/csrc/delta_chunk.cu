@@ -63,8 +63,8 @@ delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     cp_commit();
 
     if (warp == 0)
-        chunk_gates(in, ((size_t)b * in.Hv + h) * in.T + t0, len - t0, ws.gates(head, chunk), g_hi,
-                    g_lo, s_beta, nullptr, lane);
+        chunk_gates(fetch_gates(in, ((size_t)b * in.Hv + h) * in.T + t0, len - t0, lane),
+                    ws.gates(head, chunk), g_hi, g_lo, s_beta, nullptr, lane);
     cp_wait<0>();
     __syncthreads();
 
@@ -113,7 +113,7 @@ delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 // masked places are selected away, never multiplied by 0
-                const float E = expf((g_hi[i] - g_hi[j + e]) + (g_lo[i] - g_lo[j + e]));
+                const float E = exp2_sum(g_hi[i], g_lo[i], g_hi[j + e], g_lo[j + e]);
                 n[e] = i > j + e ? k2 * E * kk[nt][2 * r + e] : 0.f;
                 p[e] = i >= j + e ? qk_scale * E * qk[nt][2 * r + e] : 0.f;
                 if ((nt >> 1) == warp)

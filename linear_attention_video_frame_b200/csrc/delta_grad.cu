@@ -522,8 +522,8 @@ delta_grad_kernel(la_delta in, DeltaGrad grad, DeltaWs ws, int chunks) {
                 for (int e = 0; e < 4; ++e) {
                     const int ti = row[e >> 1], tj = ch * 32 + i * 8 + 2 * tq + (e & 1);
                     // above the diagonal E may overflow: it is selected away
-                    const float E = expf((gates[3][ti] - gates[3][tj]) +
-                                         (gates[4][ti] - gates[4][tj])) * gates[2][tj];
+                    const float E = exp2_sum(gates[3][ti], gates[4][ti], gates[3][tj],
+                                             gates[4][tj]) * gates[2][tj];
                     float p = ti >= tj ? E * dp[i][e] : 0.f;
                     float n = ti > tj ? -gates[2][ti] * E * dn[i][e] : 0.f;
 #pragma unroll

@@ -152,6 +152,48 @@ __device__ __forceinline__ void load_tile(uint32_t dst, int half, const __nv_bfl
         p += 2 * stride;
     }
 }
+// Planes of a fragment pair by pair.
+template <int NP>
+__device__ __forceinline__ void planes_of(uint32_t (&w)[NP][2][2][2], const Frag& x) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float a = x[h][j][2 * r], b = x[h][j][2 * r + 1];
+#pragma unroll
+                for (int e = 0; e < NP; ++e) {
+                    // the last of two planes is rounded: cutting errs to one side
+                    const uint32_t p = e == NP - 1 && NP < 3
+                                           ? pack_bf16(a, b)
+                                           : __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+                    w[e][h][j][r] = p;
+                    if (e < NP - 1) minus_halves(a, b, p);
+                }
+            }
+}
+// A fragment's plane (rows = value columns or tokens from r0 on, 16 columns from
+// c0 on) into a swizzled tile with the same rows ...
+__device__ __forceinline__ void put_rows(uint32_t tile, const uint32_t (&w)[2][2][2], int r0, int c0,
+                                         int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = r0 + 16 * h + 8 * ((lane >> 3) & 1) + (lane & 7), c = (c0 >> 3) + (lane >> 4);
+        stsm4(tile + r * 128 + (((c & 7) ^ (r & 7)) << 4), w[h][0][0], w[h][0][1], w[h][1][0],
+              w[h][1][1]);
+    }
+}
+// ... or transposed: the tile's rows are the fragment's columns.
+__device__ __forceinline__ void put_cols(uint32_t tile, const uint32_t (&w)[2][2][2], int r0, int c0,
+                                         int lane) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int r = c0 + 8 * j + (lane & 7), c = (r0 >> 3) + (lane >> 3);
+        stsm4_t(tile + r * 128 + (((c & 7) ^ (r & 7)) << 4), w[0][j][0], w[0][j][1], w[1][j][0],
+                w[1][j][1]);
+    }
+}
 // Asks the L2 for a run of bytes, by one warp.  (As one bulk prefetch it held up
 // the issuing thread for 5000 cycles.)
 __device__ __forceinline__ void prefetch_lines(const void* src, int bytes, int lane) {

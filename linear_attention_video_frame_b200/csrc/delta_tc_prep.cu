@@ -8,16 +8,19 @@
 // and in the backward pass dX = T^T dU = Pt^T dO + Kt dS.  With Kt and Pt a
 // chunk takes two dependent products in a chain in place of three.
 //
-// Everything beyond K K^T and Q K^T goes by blocks of 16, block column c by one
-// warp, transposed, so that the tiles of one product are the a operand of the
-// next.  L: the diagonal blocks by forward substitution (a column a lane), then
+// K K^T, Q K^T and Kt are tcgen05 products, one issue each.  What lies between goes
+// by blocks of 16 on warp-level products, block column c by one warp, transposed, so
+// that the tiles of one product are the a operand of the next.  L: the diagonal
+// blocks by forward substitution (a column a lane), then
 //     R = N_rc - sum_j N_rj (B L_jc),   L_rc = R - L_rr (B R).
-#include "delta_tiles.cuh"
+// A block is one chunk's sequence of such steps, bound by their latency: four blocks
+// share an SM.
+#include "delta_tc.cuh"
 
 namespace la {
 namespace {
+using namespace dtc;
 
-constexpr int kTri = kChunk * kChunk * 2;
 constexpr int kPacked = 10 * 512;            // a plane of the blocks up to the diagonal
 
 // 16-byte piece p (of 2) of row i of block (r, c) in a packed lower triangle.
@@ -33,17 +36,28 @@ __device__ __forceinline__ uint32_t block_cols(int r, int c, int lane) {    // a
 
 template <int DP, bool BACKWARD>
 struct PrepTc {
-    static constexpr int kTile = kChunk * DP * 2;
-    // K | Q, later P | N | L.  Forward, only L's diagonal blocks are kept (one after
-    // another), so that four blocks fit an SM.  A diagonal block of N in float32 lies
-    // where the block of L comes that is made from it.
-    static constexpr int kP3 = 3 * kPacked, kPitch = 17;
-    static constexpr int oK = 0, oP = kTile, oN = oP + (kTile > kP3 ? kTile : kP3), oL = oN + kP3;
+    // [half of the columns]: K | Q, 64 rows of 128 bytes each | planes of P that do not
+    // fit where Q was | N | L.  Forward, only L's diagonal blocks are kept (one after
+    // another).  A diagonal block of N in float32 lies where the block of L comes that
+    // is made from it.
+    static constexpr int kHalves = DP / 64, kHalf = 16384, kKQ = kHalves * kHalf;
+    static constexpr int NP = BACKWARD ? 3 : 2;             // planes of P and Pt
+    static constexpr int kExtra = NP > kHalves ? (NP - kHalves) * kPacked : 0;
+    static constexpr int kP3 = 3 * kPacked, kPitch = 20;
+    static constexpr int oN = kKQ + kExtra, oL = oN + kP3;
     static constexpr int kL = BACKWARD ? kP3 : 4 * 3 * 512;
-    static constexpr int oDiag = BACKWARD ? oL + kL : oL, kDiag = BACKWARD ? 16 * kPitch * 4 : 1536;
-    static constexpr int kBytes = BACKWARD ? oDiag + 4 * kDiag : oL + kL;
-    // staging of Pt (over N and L) and of half of Kt's columns (over P and N)
-    static_assert(kP3 + kL >= (BACKWARD ? 3 : 2) * kTri && oL - oP >= 3 * 8192, "staging");
+    static constexpr int oDiag = BACKWARD ? oL + kL : oL, kDiag = 1536;
+    static constexpr int kEnd = BACKWARD ? oDiag + 4 * kDiag : oL + kL, kBytes = kEnd + 1024;
+    static __device__ __forceinline__ constexpr int plane_p(int e) {
+        return e < kHalves ? e * kHalf + 8192 : kKQ + (e - kHalves) * kPacked;
+    }
+    // planes of M = k_scale tail o (I - B L), 8192 bytes each: where Q (and P) were, and
+    // over N and L; Pt is staged over N and L before
+    static __device__ __forceinline__ constexpr int plane_m(int e) {
+        return e < kHalves ? e * kHalf + 8192 : oN + (e - kHalves) * 8192;
+    }
+    static_assert(kP3 + kL >= NP * kTri && kP3 + kL >= (3 - kHalves) * 8192, "staging");
+    static_assert(kEnd >= kHalves * 3 * 8192, "staging of Kt, from the start");
     // a plane of L, and its block (r, r)
     static constexpr int kPlaneL = BACKWARD ? kPacked : 512;
     static __device__ __forceinline__ int block(int r) {
@@ -51,106 +65,174 @@ struct PrepTc {
     }
 };
 
+// A wait of this kernel, which starts before the status word is known to be reset.
+__device__ __forceinline__ void wait_bounded(uint64_t* bar, uint32_t parity, unsigned int* status) {
+    if (tc::mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = tc::global_timer_ns();
+    while (!tc::mbar_try_wait(bar, parity))
+        if (tc::global_timer_ns() - t0 > tc::kWaitLimitNs) {
+            atomicExch(status, (unsigned)LA_ERR_TIMEOUT);
+            return;
+        }
+}
+
 template <int DP, bool BACKWARD>
 __global__ void __launch_bounds__(128, BACKWARD ? 3 : 4)
 delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     using Sm = PrepTc<DP, BACKWARD>;
-    constexpr int CH = DP / 8;
-    extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float g_hi[kChunk], g_lo[kChunk], s_beta[kChunk], s_tail[kChunk];
+    constexpr int NP = Sm::NP;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = tc::align1024(smem_raw);
+    __shared__ __align__(16) float g_hi[kChunk], g_lo[kChunk], s_beta[kChunk], s_tail[kChunk];
+    __shared__ uint64_t done;
+    __shared__ uint32_t s_tmem;
 
     const int chunk = blockIdx.x % chunks, head = blockIdx.x / chunks;
-    const int b = head / in.Hv, h = head % in.Hv, hk = h / (in.Hv / in.Hk);
+    const int b = head / in.Hv, h = head % in.Hv, hk = h / (in.Hv / in.Hk), D = in.D;
     const int len = seq_len(in.lengths, b, in.T);
-    const int t0 = chunk * kChunk;
+    const int t0 = chunk * kChunk, rows = len - t0;
     const int tid = threadIdx.x, lane = tid & 31;
+    const int wid = __shfl_sync(~0u, tid >> 5, 0);
     // block column 0 has the most to do: its warp differs from block to block
-    const int warp = ((tid >> 5) + blockIdx.x) & 3;
+    const int warp = (wid + blockIdx.x) & 3;
     if (blockIdx.x == 0 && tid < 2) ws.status[tid] = 0;
-    if (t0 >= len) return;
+    if (rows <= 0) return;
     const uint32_t base = smem_u32(smem);
-    const uint32_t sK = base + Sm::oK, sQ = base + Sm::oP, sP = sQ, sN = base + Sm::oN,
-                   sL = base + Sm::oL;
-    float* diag = reinterpret_cast<float*>(smem + Sm::oDiag + warp * Sm::kDiag);
+    const uint32_t sN = base + Sm::oN, sL = base + Sm::oL;
     const int g = lane >> 2, tq = lane & 3;
 
-    load_rows<DP>(sK, in.k, row3(in.k_stride).at(b, hk, 0), in.k_stride[2], t0, len, in.D,
-                         tid, 128);
-    load_rows<DP>(sQ, in.q, row3(in.q_stride).at(b, hk, 0), in.q_stride[2], t0, len, in.D,
-                         tid, 128);
-    cp_commit();
-    if (warp == 3)
-        chunk_gates(in, ((size_t)b * in.Hv + h) * in.T + t0, len - t0, ws.gates(head, chunk), g_hi,
-                    g_lo, s_beta, s_tail, lane);
-    cp_wait<0>();
-    __syncthreads();
-
-    // Rows 16 w .. 16 w + 15 of K K^T and Q K^T, up to the diagonal.
-    float kk[8][4], qk[8][4];
+    RawGates raw;                     // asked for first: the sums over them take longest
+    if (wid == 3) raw = fetch_gates(in, ((size_t)b * in.Hv + h) * in.T + t0, rows, lane);
+    // K and Q, blocks of 16 rows in the order 0 3 1 2: lanes of the products are rows, and
+    // so each warp has five blocks of 16 x 16 up to the diagonal.  Two warps each, their
+    // own lanes' rows.
+    const int rb[2] = {wid & 1, 3 - (wid & 1)};
+    {
+        const Row3 r3 = row3(wid < 2 ? in.k_stride : in.q_stride);
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(wid < 2 ? in.k : in.q) +
+                                   r3.at(b, hk, t0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) kk[i][e] = qk[i][e] = 0.f;
-#pragma unroll 2
-    for (int ks = 0; ks < DP / 16; ++ks) {
-        uint32_t ak[4], aq[4];
-        ldsm4(ak, at_rows<CH>(sK, warp * 16, 2 * ks, lane));
-        ldsm4(aq, at_rows<CH>(sQ, warp * 16, 2 * ks, lane));
-#pragma unroll
-        for (int np = 0; np < 4; ++np) {
-            if (np > warp) break;
-            uint32_t bk[4];
-            ldsm4(bk, at_cols<CH>(sK, np * 16, 2 * ks, lane));
-            mma_bf16(kk[2 * np], ak, bk[0], bk[1]);
-            mma_bf16(kk[2 * np + 1], ak, bk[2], bk[3]);
-            mma_bf16(qk[2 * np], aq, bk[0], bk[1]);
-            mma_bf16(qk[2 * np + 1], aq, bk[2], bk[3]);
+        for (int hh = 0; hh < 2; ++hh) {
+            const int first = 16 * rb[hh];
+            load_tile<16>(base + (wid >> 1) * 8192 + (32 * (wid & 1) + 16 * hh) * 128, Sm::kHalf,
+                          rows > first ? src + first * r3.t : src, r3.t, rows - first, D, lane);
         }
+        cp_commit();
     }
-    __syncthreads();                  // Q has been read
-    const float k2 = in.k_scale * in.k_scale, qk_scale = in.k_scale * in.q_scale;
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-        if (nt >= 2 * (warp + 1)) break;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int i = warp * 16 + g + 8 * r, j = nt * 8 + 2 * tq;
-            float n[2], p[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                // masked places are selected away, never multiplied by 0
-                const float E = expf((g_hi[i] - g_hi[j + e]) + (g_lo[i] - g_lo[j + e]));
-                n[e] = i > j + e ? k2 * E * kk[nt][2 * r + e] : 0.f;
-                p[e] = i >= j + e ? qk_scale * E * qk[nt][2 * r + e] : 0.f;
-                if ((nt >> 1) == warp)
-                    diag[(i & 15) * Sm::kPitch + ((j + e) & 15)] = n[e];
-            }
-            uint32_t wn[3], wp[3];
-            cut_planes(n[0], n[1], wn);
-            cut_planes(p[0], p[1], wp);
-            const uint32_t at = packed_at(warp, nt >> 1, i & 15, nt & 1) + 4 * tq;
-#pragma unroll
-            for (int e = 0; e < 3; ++e) {
-                *reinterpret_cast<uint32_t*>(smem + Sm::oP + e * kPacked + at) = wp[e];
-                *reinterpret_cast<uint32_t*>(smem + Sm::oN + e * kPacked + at) = wn[e];
-            }
+    if (wid == 0) {
+        if (lane == 0) {
+            tc::mbar_init(&done, 1);
+            tc::fence_mbar_init();
         }
+        __syncwarp();
+        tc::tmem_alloc(&s_tmem, 64);
+        tc::tmem_relinquish();
+    }
+    if (wid == 3)
+        chunk_gates(raw, ws.gates(head, chunk), g_hi, g_lo, s_beta, s_tail, lane);
+    cp_wait<0>();
+    tc::fence_proxy_async_smem();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tm = __shfl_sync(~0u, s_tmem, 0);
+    if (wid == 0 && tc::elect_one()) {          // [K; Q] K^T: lanes 0 .. 63 and 64 .. 127
+        const Desc k(base, 0, 1024);
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i)
+            if (i < D / 16) {
+                const uint64_t d = k.at((i >> 2) * Sm::kHalf + (i & 3) * 32);
+                tc::mma_bf16(tm, d, d, tc::idesc_bf16(128, 64, false, false), i > 0);
+            }
+        tc::mma_commit(&done);
     }
     __syncwarp();
-    // this warp's diagonal block: column `lane`
+    wait_bounded(&done, 0, ws.status);
+    tc::tc_fence_after();
+
+    // N (warps 0 and 1) and P (2 and 3), 32 rows each, up to the diagonal
+    const float scale = in.k_scale * (wid < 2 ? in.k_scale : in.q_scale);
+    const uint32_t at = tc::tmem_addr(tm, wid * 32, 0);
+    float row_hi[2][2], row_lo[2][2];
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            row_hi[hh][r] = g_hi[rb[hh] * 16 + 8 * r + g];
+            row_lo[hh][r] = g_lo[rb[hh] * 16 + 8 * r + g];
+        }
+#pragma unroll 1
+    for (int cb = 0; cb <= rb[1]; ++cb) {
+        Factors col_hi, col_lo;
+        factors(col_hi, g_hi + cb * 16, tq);
+        factors(col_lo, g_lo + cb * 16, tq);
+        Frag x;
+        load_frag(x, at + (cb == 0 ? 0 : cb == 3 ? 1 : cb + 1) * 16);     // where block cb is
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            if (cb > rb[hh]) continue;
+            uint32_t w[3][2][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int ti = rb[hh] * 16 + 8 * r + g, tj = cb * 16 + 8 * j + 2 * tq;
+                    float y[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        // masked places are selected away, never multiplied by 0
+                        const float E = exp2_sum(row_hi[hh][r], row_lo[hh][r], factor(col_hi, j, e),
+                                                 factor(col_lo, j, e));
+                        const bool on = wid < 2 ? ti > tj + e : ti >= tj + e;
+                        y[e] = on ? scale * E * x[hh][j][2 * r + e] : 0.f;
+                    }
+                    uint32_t p[3];
+                    if (NP == 2 && wid >= 2) {
+                        uint32_t q[2];
+                        split_bf16<2>(y[0], y[1], q);
+                        p[0] = q[0];
+                        p[1] = q[1];
+                        p[2] = 0;
+                    } else {
+                        cut_planes(y[0], y[1], p);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) w[e][j][r] = p[e];
+                    if (wid < 2 && cb == rb[hh]) {
+                        float* diag = reinterpret_cast<float*>(smem + Sm::oDiag + cb * Sm::kDiag);
+                        *reinterpret_cast<float2*>(diag + (8 * r + g) * Sm::kPitch + 8 * j + 2 * tq) =
+                            make_float2(y[0], y[1]);
+                    }
+                }
+            const uint32_t to = packed_at(rb[hh], cb, (lane & 7) + 8 * ((lane >> 3) & 1), lane >> 4);
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+                if (wid >= 2 && e >= NP) break;
+                const uint32_t plane = wid < 2 ? sN + e * kPacked : base + Sm::plane_p(e);
+                stsm4(plane + to, w[e][0][0], w[e][0][1], w[e][1][0], w[e][1][1]);
+            }
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    // the diagonal blocks of L: column `lane` of this warp's
     {
-        const float* n = diag;
+        const float* n = reinterpret_cast<const float*>(smem + Sm::oDiag + warp * Sm::kDiag);
         const int c = lane & 15;
         float l[16], bl[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float s0 = 0.f, s1 = 0.f;
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < i; ++j) {
-                if (j & 1) s1 += n[i * Sm::kPitch + j] * bl[j];
-                else s0 += n[i * Sm::kPitch + j] * bl[j];
+            for (int j = 0; j < i; j += 4) {
+                const float4 q = *reinterpret_cast<const float4*>(n + i * Sm::kPitch + j);
+                const float f[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (j + e < i) s[e] += f[e] * bl[j + e];
             }
-            l[i] = i > c ? n[i * Sm::kPitch + c] - (s0 + s1) : 0.f;
+            l[i] = i > c ? n[i * Sm::kPitch + c] - ((s[0] + s[1]) + (s[2] + s[3])) : 0.f;
             bl[i] = s_beta[warp * 16 + i] * l[i];
         }
         __syncwarp();                 // all of the block has been read
@@ -273,7 +355,6 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     __syncthreads();                  // N and L have been read: Pt is staged over them
 
     // Pt = P - P B L; outputs in bf16 need two planes of it, states' gradients three
-    constexpr int NP = BACKWARD ? 3 : 2;
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
         const int i = warp + d;
@@ -285,14 +366,14 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
         for (int r = 0; r <= d; ++r) {
             uint32_t p[3][4];
 #pragma unroll
-            for (int e = 0; e < NP; ++e) ldsm4(p[e], sP + e * kPacked + block_cols(i, warp + r, lane));
+            for (int e = 0; e < NP; ++e) ldsm4(p[e], base + Sm::plane_p(e) + block_cols(i, warp + r, lane));
             product_planes<NP, 3, 3>(C, bl[r], p);
         }
         float R[2][4] = {};
 #pragma unroll
-        for (int e = 2; e >= 0; --e) {
+        for (int e = NP - 1; e >= 0; --e) {
             uint32_t w[4];
-            ldsm4_t(w, sP + e * kPacked + block_rows(i, warp, lane));
+            ldsm4_t(w, base + Sm::plane_p(e) + block_rows(i, warp, lane));
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -320,15 +401,14 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
                         w[0][e], w[1][e]);
         }
     }
+    tc::fence_proxy_async_smem();
     __syncthreads();
-    {
-        unsigned char* out = reinterpret_cast<unsigned char*>(ws.P(head, chunk));
-        for (int i = tid; i < NP * kTri / 16; i += 128)
-            reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(smem + Sm::oN)[i];
+    if (wid == 0 && lane == 0) {
+        tc::bulk_store(ws.P(head, chunk), smem + Sm::oN, NP * kTri);
+        tc::bulk_commit();
     }
 
-    __syncthreads();                  // Pt has left, P has been read: Kt is staged there
-    // (B L)^T to k_scale (tail o (I - B L))^T
+    // (B L)^T to M^T = k_scale (tail o (I - B L))^T, and M's rows as operand tiles
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
         const int r = warp + d;
@@ -353,41 +433,63 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
             for (int e = 0; e < 3; ++e) bl[d][e][i] = p[e];
         }
     }
-    // Kt, 64 columns at a time: rows 16 w .. 16 w + 15
-#pragma unroll 1
-    for (int half = 0; half < DP / 64; ++half) {
-        if (half > 0) __syncthreads();      // the staged values before have left
-        unsigned char* stage = smem + Sm::oP;
-#pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-            Acc C[4];
+    if (wid == 0 && lane == 0) tc::bulk_wait_read<0>();
+    __syncthreads();                  // Pt has left
 #pragma unroll
-            for (int j = 0; j < 4; ++j) C[j].zero();
+    for (int d = 0; d < 4; ++d) {
+        const int r = warp + d;
+        if (r > 3) break;
+        const int row = (r == 0 ? 0 : r == 3 ? 1 : r + 1) * 16 + 8 * (lane >> 4) + (lane & 7),
+                  c = 2 * warp + ((lane >> 3) & 1);
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                const int r = warp + d;
-                if (r > 3) break;
+        for (int e = 0; e < 3; ++e)
+            stsm4_t(base + Sm::plane_m(e) + row * 128 + ((c ^ (row & 7)) << 4), bl[d][e][0],
+                    bl[d][e][1], bl[d][e][2], bl[d][e][3]);
+    }
+    tc::fence_proxy_async_smem();
+    __syncthreads();
+    if (wid == 0 && tc::elect_one()) {          // Kt^T = K^T M, block row r of M up to its diagonal
+        tc::tc_fence_after();
+        const Desc a(base, DP == 64 ? 0 : Sm::kHalf, 1024);
 #pragma unroll
-                for (int np = 0; np < 2; ++np)
-                    product_rows<3, 3, 1, CH>(C + 2 * np, bl[d], sK, Sm::kTile, r * 16,
-                                              half * 8 + 4 * q + 2 * np, lane);
+        for (int e = 2; e >= 0; --e) {
+            const Desc m(base + Sm::plane_m(e), 0, 1024);
+#pragma unroll
+            for (int r = 3; r >= 0; --r) {      // the widest first: it sets all columns
+                const int p = r == 0 ? 0 : r == 3 ? 1 : r + 1;
+                tc::mma_bf16(tm, a.at(p * 2048), m.at(p * 2048),
+                             tc::idesc_bf16(128, 16 * r + 16, true, true), e < 2 || r < 3);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    uint32_t w[3];
-                    cut_planes(C[j][2 * r], C[j][2 * r + 1], w);
-                    const uint32_t at = tile_at<8>(warp * 16 + g + 8 * r, 4 * q + j) + 4 * tq;
-#pragma unroll
-                    for (int e = 0; e < 3; ++e)
-                        *reinterpret_cast<uint32_t*>(stage + e * 8192 + at) = w[e];
-                }
         }
-        __syncthreads();
-        unsigned char* out = ws.Kt(head, chunk) + half * 3 * 8192;
-        for (int i = tid; i < 3 * 8192 / 16; i += 128)
-            reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(stage)[i];
+        tc::mma_commit(&done);
+    }
+    __syncwarp();
+    wait_bounded(&done, 1, ws.status);
+    tc::tc_fence_after();
+    // its planes as rows of tokens, over everything
+    if (wid < DP / 32)
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            Frag x;
+            load_frag(x, at + 16 * i);
+            tc::tmem_wait_ld();
+            uint32_t w[3][2][2][2];
+            planes_of<3>(w, x);
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                put_cols(base + ((wid >> 1) * 3 + e) * 8192, w[e], 32 * (wid & 1), 16 * i, lane);
+        }
+    tc::fence_proxy_async_smem();
+    tc::tc_fence_before();
+    __syncthreads();
+    if (wid == 0) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tm, 64);
+        if (lane == 0) {
+            tc::bulk_store(ws.Kt(head, chunk), smem, Sm::kHalves * 3 * 8192);
+            tc::bulk_commit();
+            tc::bulk_wait_read<0>();
+        }
     }
 }
 

@@ -12,7 +12,7 @@ namespace la {
 // three as well.
 constexpr int kPlanes = 3;
 
-// Per token: exp(G), exp(G_63 - G), beta, and G as the sum of two floats.
+// Per token: exp(G), exp(G_63 - G), beta, and G / ln 2 as the sum of two floats.
 constexpr int kGateRows = 5;
 
 // A head's chain may be cut into segments of chunks (bf16 inputs): with few heads
@@ -277,21 +277,35 @@ __device__ __forceinline__ void product_rows(Acc* c, const uint32_t (&a)[NA][4],
     product_planes<NP, NA, NB>(c, a, b);
 }
 
-// The gates of a chunk's 64 tokens, by one warp.  Running sums of log_alpha in
-// double, kept as two floats: differences of sums far from 0 keep the accuracy
-// of their own size.  Tokens from `on` on have alpha = 1 and beta = 0.
-__device__ __forceinline__ void chunk_gates(const la_delta& in, size_t at, int on, float* gates,
-                                            float* g_hi, float* g_lo, float* beta, float* tail,
-                                            int lane) {
-    double s[2];
-    float bt[2];
+// The gates of a chunk's 64 tokens, by one warp: log_alpha and beta of tokens
+// 2 lane, 2 lane + 1 (those from `on` on have alpha = 1 and beta = 0) ...
+// 2^((a_hi - b_hi) + (a_lo - b_lo)) to 2 units in the last place.
+__device__ __forceinline__ float exp2_sum(float a_hi, float a_lo, float b_hi, float b_lo) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((a_hi - b_hi) + (a_lo - b_lo)));
+    return y;
+}
+struct RawGates { float g[2], beta[2]; };
+__device__ __forceinline__ RawGates fetch_gates(const la_delta& in, size_t at, int on, int lane) {
+    RawGates r;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t = 2 * lane + i;
-        const float g = t < on ? in.log_alpha[at + t] : 0.f;
-        s[i] = g < kLogAlphaMin ? kLogAlphaMin : g;         // keeps NaN
-        bt[i] = t < on ? in.beta[at + t] : 0.f;
+        r.g[i] = t < on ? in.log_alpha[at + t] : 0.f;
+        r.beta[i] = t < on ? in.beta[at + t] : 0.f;
     }
+    return r;
+}
+// ... and what follows from them.  Running sums of log_alpha in double, kept in
+// powers of two as two floats: differences of sums far from 0 keep the accuracy of
+// their own size, and exp2_sum takes them as they are.
+__device__ __forceinline__ void chunk_gates(const RawGates& raw, float* gates, float* g_hi,
+                                            float* g_lo, float* beta, float* tail, int lane) {
+    double s[2];
+    const float* bt = raw.beta;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        s[i] = raw.g[i] < kLogAlphaMin ? kLogAlphaMin : raw.g[i];      // keeps NaN
     s[1] += s[0];
     double run = s[1];
 #pragma unroll
@@ -305,13 +319,14 @@ __device__ __forceinline__ void chunk_gates(const la_delta& in, size_t at, int o
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t = 2 * lane + i;
-        const float hi = (float)s[i], lo = (float)(s[i] - (double)hi);
+        const double p = s[i] * 1.4426950408889634;
+        const float hi = (float)p, lo = (float)(p - (double)hi);
         const float to_end = expf((float)(last - s[i]));
         g_hi[t] = hi;
         g_lo[t] = lo;
         beta[t] = bt[i];
         if (tail) tail[t] = to_end;
-        gates[t] = expf(hi);
+        gates[t] = expf((float)s[i]);
         gates[kChunk + t] = to_end;
         gates[2 * kChunk + t] = bt[i];
         gates[3 * kChunk + t] = hi;
