@@ -26,22 +26,54 @@ namespace {
 //     R = N_rc - sum_j N_rj (B L_jc),   L_rc = R - L_rr (B R),
 // on tensor cores, transposed so that a block's result tiles are the next
 // product's a operand; the serial part is 16 rows in place of 64.
-template <int DP>
+//
+// K and Q come 64 columns at a time, so that three blocks share an SM.
 struct PrepSmem {
-    static constexpr int kTile = kChunk * DP * 2, kTri = kChunk * kChunk * 2;
+    static constexpr int kTile = kChunk * 128, kTri = kChunk * kChunk * 2;
     static constexpr int NI = kPlanes, NP = kPlanes;
-    // K and Q, later P, later L; N; the diagonal blocks of N in float32
-    static constexpr int kQ = NI * kTile;
-    static constexpr int kKQ = 2 * kQ > NP * kTri ? 2 * kQ : NP * kTri;
-    static constexpr int kN = kKQ, kDiag = kN + NP * kTri, kPitch = 17;
+    // K and Q, later P, later L, and N; the diagonal blocks of N in float32
+    static constexpr int kQ = NI * kTile, kN = kQ, kDiag = 2 * kQ, kPitch = 17;
+    static_assert(kTri <= kTile, "P and N take the place of K and Q");
     static constexpr int kBytes = kDiag + 4 * 16 * kPitch * 4;
 };
 
+// 64 columns of rows t0 .. of a float32 matrix as tiles of planes, and, where `planes`
+// is given, as pieces first .. of tiles of DP columns there.
 template <int DP>
-__global__ void __launch_bounds__(128)
+__device__ __forceinline__ void load_half(uint32_t dst, const float* src, long long stride, int t0,
+                                          int len, int columns, unsigned char* planes, int first,
+                                          int tid) {
+#pragma unroll
+    for (int i = tid; i < kChunk * 8; i += 128) {
+        const int r = i >> 3, c = i & 7;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (t0 + r < len && c * 8 < columns) {
+            const float4* p = reinterpret_cast<const float4*>(src + (t0 + r) * stride + c * 8);
+            x = p[0];
+            y = p[1];
+        }
+        const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        uint32_t w[4][kPlanes];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_bf16<kPlanes>(f[2 * e], f[2 * e + 1], w[e]);
+#pragma unroll
+        for (int j = 0; j < kPlanes; ++j) {
+            const uint4 v = make_uint4(w[0][j], w[1][j], w[2][j], w[3][j]);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};"
+                         :: "r"(dst + j * PrepSmem::kTile + tile_at<8>(r, c)), "r"(v.x), "r"(v.y),
+                            "r"(v.z), "r"(v.w) : "memory");
+            if (planes)
+                *reinterpret_cast<uint4*>(planes + j * kChunk * DP * 2 +
+                                          tile_at<DP / 8>(r, first + c)) = v;
+        }
+    }
+}
+
+template <int DP>
+__global__ void __launch_bounds__(128, 3)
 delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
-    using Sm = PrepSmem<DP>;
-    constexpr int CH = DP / 8, NI = Sm::NI, NP = Sm::NP, kTri = Sm::kTri;
+    using Sm = PrepSmem;
+    constexpr int NI = Sm::NI, NP = Sm::NP, kTri = Sm::kTri;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float g_hi[kChunk], g_lo[kChunk], s_beta[kChunk];
 
@@ -56,23 +88,9 @@ delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     const uint32_t sK = base, sQ = base + Sm::kQ, sN = base + Sm::kN;
     float* diag = reinterpret_cast<float*>(smem + Sm::kDiag);
 
-    load_rows_split<DP>(sK, in.k, row3(in.k_stride).at(b, hk, 0), in.k_stride[2], t0, len, in.D,
-                       tid, 128);
-    load_rows_split<DP>(sQ, in.q, row3(in.q_stride).at(b, hk, 0), in.q_stride[2], t0, len, in.D,
-                       tid, 128);
-    cp_commit();
-
     if (warp == 0)
         chunk_gates(fetch_gates(in, ((size_t)b * in.Hv + h) * in.T + t0, len - t0, lane),
                     ws.gates(head, chunk), g_hi, g_lo, s_beta, nullptr, lane);
-    cp_wait<0>();
-    __syncthreads();
-
-    if (h % ratio == 0) {      // the planes of k and q that the chains load
-        unsigned char* out = ws.planes(b * in.Hk + hk, chunk);
-        for (int i = tid; i < 2 * Sm::kQ / 16; i += 128)
-            reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(smem)[i];
-    }
 
     // Warp w: rows 16 w .. 16 w + 15 of Kh Kh^T and Qh Kh^T, up to the diagonal.
     Acc kk[8], qk[8];
@@ -81,23 +99,36 @@ delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
         kk[i].zero();
         qk[i].zero();
     }
+    const float* pk = static_cast<const float*>(in.k) + row3(in.k_stride).at(b, hk, 0);
+    const float* pq = static_cast<const float*>(in.q) + row3(in.q_stride).at(b, hk, 0);
+    // the planes of k and q that the chains load
+    unsigned char* out = h % ratio == 0 ? ws.planes(b * in.Hk + hk, chunk) : nullptr;
 #pragma unroll 1
-    for (int ks = 0; ks < DP / 16; ++ks) {
-        uint32_t ak[NI][4], aq[NI][4];
+    for (int half = 0; half < DP / 64; ++half) {
+        if (half) __syncthreads();
+        load_half<DP>(sK, pk + 64 * half, in.k_stride[2], t0, len, in.D - 64 * half, out, 8 * half,
+                      tid);
+        load_half<DP>(sQ, pq + 64 * half, in.q_stride[2], t0, len, in.D - 64 * half,
+                      out ? out + NI * kChunk * DP * 2 : nullptr, 8 * half, tid);
+        __syncthreads();
+#pragma unroll 1
+        for (int ks = 0; ks < 4; ++ks) {
+            uint32_t ak[NI][4], aq[NI][4];
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            ldsm4(ak[i], at_rows<CH>(sK + i * Sm::kTile, warp * 16, 2 * ks, lane));
-            ldsm4(aq[i], at_rows<CH>(sQ + i * Sm::kTile, warp * 16, 2 * ks, lane));
-        }
+            for (int i = 0; i < NI; ++i) {
+                ldsm4(ak[i], at_rows<8>(sK + i * Sm::kTile, warp * 16, 2 * ks, lane));
+                ldsm4(aq[i], at_rows<8>(sQ + i * Sm::kTile, warp * 16, 2 * ks, lane));
+            }
 #pragma unroll
-        for (int np = 0; np < 4; ++np) {
-            if (np > warp) break;
-            uint32_t bk[NI][4];
+            for (int np = 0; np < 4; ++np) {
+                if (np > warp) break;
+                uint32_t bk[NI][4];
 #pragma unroll
-            for (int j = 0; j < NI; ++j)
-                ldsm4(bk[j], at_cols<CH>(sK + j * Sm::kTile, np * 16, 2 * ks, lane));
-            product_planes<NI, NI, NI>(kk + 2 * np, ak, bk);
-            product_planes<NI, NI, NI>(qk + 2 * np, aq, bk);
+                for (int j = 0; j < NI; ++j)
+                    ldsm4(bk[j], at_cols<8>(sK + j * Sm::kTile, np * 16, 2 * ks, lane));
+                product_planes<NI, NI, NI>(kk + 2 * np, ak, bk);
+                product_planes<NI, NI, NI>(qk + 2 * np, aq, bk);
+            }
         }
     }
     __syncthreads();                  // K and Q have been read
@@ -132,9 +163,9 @@ delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     }
     __syncthreads();
     {
-        unsigned char* out = reinterpret_cast<unsigned char*>(ws.P(head, chunk));
+        unsigned char* to = reinterpret_cast<unsigned char*>(ws.P(head, chunk));
         for (int i = tid; i < NP * kTri / 16; i += 128)
-            reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(smem)[i];
+            reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(smem)[i];
     }
     // the diagonal block of warp's rows: column `lane`
     float l[16];
@@ -240,9 +271,9 @@ delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
         if (d < 3) split_tiles<NP>(X[0], X[1], bl[d]);
     }
     __syncthreads();
-    unsigned char* out = reinterpret_cast<unsigned char*>(ws.L(head, chunk));
+    unsigned char* to = reinterpret_cast<unsigned char*>(ws.L(head, chunk));
     for (int i = tid; i < NP * kTri / 16; i += 128)
-        reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(smem)[i];
+        reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(smem)[i];
 }
 
 // ---------------------------------------------------------------------------
@@ -260,33 +291,31 @@ delta_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
 // products of 8 cycles each.  KS warps therefore share a slice's key rows (each
 // holds DP / KS of them): their partial sums of Kh S and Qh S meet in shared
 // memory, the middle part is computed by each, the outputs are split between
-// them by token.
-template <int DP, int KS, int SL, int STAGES, bool STATES>
+// them by token.  Their steps leave most of an SM's time unused, so that two blocks
+// share it: Q and K, and L and P, come one after the other to the same place.
+template <int DP, int KS, bool STATES>
 struct ChainSmem {
     static constexpr int kTile = kChunk * DP * 2;                 // a plane of K or Q
     static constexpr int kLP = kChunk * kChunk * 2;               // a plane of L or P
-    static constexpr int kV = ValueTile<SL>::kBytes;
     static constexpr int kGates = 3 * kChunk * 4;
-    // offsets in a stage
     static constexpr int oK = 0, oL = oK + kPlanes * kTile, oV = oL + kPlanes * kLP,
-                         oGates = oV + kV, oQ = oGates + kGates,
-                         oP = oQ + (STATES ? 0 : kPlanes * kTile),
-                         kStage = oP + (STATES ? 0 : kPlanes * kLP);
-    static constexpr int oExchange = STAGES * kStage;
+                         oGates = oV + ValueTile::kBytes;      // of two chunks
+    static constexpr int oExchange = oGates + 2 * kGates;
     // per warp: partial sums, 8 tiles of 512 bytes (twice with outputs)
-    static constexpr int kExchange = KS > 1 ? KS * SL * 8 * 512 * (STATES ? 1 : 2) : 0;
+    static constexpr int kExchange = KS * 8 * 512 * (STATES ? 1 : 2);
     static constexpr int oOut = oExchange + kExchange;
-    static constexpr int kOut = STATES ? KS * SL * kChunk * 32 : 0;
+    static constexpr int kOut = STATES ? kChunk * 32 : 0;
     static constexpr int kBytes = oOut + kOut;
+    static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two blocks on an SM");
 };
 
 // STATES: instead of outputs, the starting state of every chunk and the final
 // one (as split S^T images) and Z (split) are written, for the backward pass.
-template <int DP, int KS, int SL, int STAGES, bool STATES>
-__global__ void __launch_bounds__(32 * KS * SL)
+template <int DP, int KS, bool STATES>
+__global__ void __launch_bounds__(32 * KS, 2)
 delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) {
-    using Sm = ChainSmem<DP, KS, SL, STAGES, STATES>;
-    constexpr int THREADS = 32 * KS * SL;
+    using Sm = ChainSmem<DP, KS, STATES>;
+    constexpr int THREADS = 32 * KS;
     constexpr int CH = DP / 8;            // 16-byte pieces of a K row
     constexpr int DK = DP / KS;           // key rows of a warp
     constexpr int NT = DK / 8;            // tiles of S^T in a warp
@@ -294,14 +323,11 @@ delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) 
     extern __shared__ __align__(128) unsigned char smem[];
     const uint32_t base = smem_u32(smem);
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int slice = warp / KS, part = warp % KS;
+    const int tid = threadIdx.x, lane = tid & 31, part = tid >> 5;
     const int g = lane >> 2, tq = lane & 3;
     const int head = blockIdx.x, b = head / in.Hv, h = head % in.Hv, hk = h / (in.Hv / in.Hk);
     const int D = in.D;
-    const int vb = blockIdx.y * SL * 16;      // first value column of the block
-    const int v0 = vb + slice * 16;           // of the warp
-    const bool live = v0 < D;                 // D is a multiple of 16
+    const int v0 = blockIdx.y * 16;           // first value column; D is a multiple of 16
     const int k0 = part * DK;
     const int len = seq_len(in.lengths, b, in.T);
     const int nc = (len + kChunk - 1) / kChunk;
@@ -314,99 +340,78 @@ delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) 
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int dk = k0 + nt * 8 + 2 * tq + (e & 1), v = v0 + g + 8 * (e >> 1);
-                S[nt][e] = s_in && live && dk < D ? s_in[(size_t)dk * D + v] : 0.f;
+                S[nt][e] = s_in && dk < D ? s_in[(size_t)dk * D + v] : 0.f;
             }
     }
 
-    auto load = [&](int c, int stage) {
-        const uint32_t st = base + stage * Sm::kStage;
-        const int t0 = c * kChunk;
-        const unsigned char* planes = ws.planes(b * in.Hk + hk, c);
-        copy_bytes(st + Sm::oK, planes, NI * Sm::kTile, tid, THREADS);
-        if constexpr (!STATES)
-            copy_bytes(st + Sm::oQ, planes + NI * Sm::kTile, NI * Sm::kTile, tid, THREADS);
-        load_values<SL>(st + Sm::oV, in.v, row3(in.v_stride).at(b, h, 0), in.v_stride[2], vb,
-                             t0, len, D, tid, THREADS);
-        copy_bytes(st + Sm::oL, ws.L(head, c), NP * Sm::kLP, tid, THREADS);
-        if constexpr (!STATES) copy_bytes(st + Sm::oP, ws.P(head, c), NP * Sm::kLP, tid, THREADS);
-        copy_bytes(st + Sm::oGates, ws.gates(head, c), Sm::kGates, tid, THREADS);
+    // the first of what the K place holds, V and the gates
+    auto load = [&](int c) {
+        copy_bytes(base + Sm::oK, ws.planes(b * in.Hk + hk, c) + (STATES ? 0 : NI * Sm::kTile),
+                   NI * Sm::kTile, tid, THREADS);
+        load_values(base + Sm::oV, in.v, row3(in.v_stride).at(b, h, 0), in.v_stride[2], v0,
+                       c * kChunk, len, tid, THREADS);
+        copy_bytes(base + Sm::oGates + (c & 1) * Sm::kGates, ws.gates(head, c), Sm::kGates, tid,
+                   THREADS);
         cp_commit();
     };
 
-    if (STAGES > 1 && nc > 0) load(0, 0);
+    if (nc > 0) load(0);
     for (int c = 0; c < nc; ++c) {
-        const int stage = STAGES > 1 ? c & 1 : 0;
-        if (STAGES > 1) {
-            cp_wait<0>();
-            __syncthreads();        // the chunk has landed; the other stage is free
-            if (c + 1 < nc) load(c + 1, stage ^ 1);
-        } else {
-            __syncthreads();        // the stage is free
-            load(c, 0);
-            cp_wait<0>();
-            __syncthreads();
-        }
-        const uint32_t st = base + stage * Sm::kStage;
-        const float* gates = reinterpret_cast<const float*>(smem + stage * Sm::kStage + Sm::oGates);
+        const float* gates =
+            reinterpret_cast<const float*>(smem + Sm::oGates + (c & 1) * Sm::kGates);
+        cp_wait<0>();
+        __syncthreads();            // it has landed; L's place is free
+        copy_bytes(base + Sm::oL, ws.L(head, c), NP * Sm::kLP, tid, THREADS);
+        cp_commit();
 
-        if constexpr (STATES)
-            if (live) store_image<NP>(ws.states(head, c), S, v0, k0, DP, D, lane);
+        if constexpr (STATES) store_image<NP>(ws.states(head, c), S, v0, k0, DP, D, lane);
 
-        // (Kh S0)^T and (Qh S0)^T, this warp's key rows
+        // (Qh S0)^T and (Kh S0)^T, this warp's key rows; every warp adds the parts up in
+        // the same order
         float M[8][4], O[8][4];
-        Acc m[8], q[8];
+        float4* ex = reinterpret_cast<float4*>(smem + Sm::oExchange);
+        float4* exo = ex + KS * 256;
+        auto by_state = [&](float4* to) {
+            Acc m[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            m[i].zero();
-            q[i].zero();
+            for (int i = 0; i < 8; ++i) m[i].zero();
+#pragma unroll
+            for (int ks = 0; ks < DK / 16; ++ks) {
+                uint32_t a[NP][4];
+                split_tiles<NP>(S[2 * ks], S[2 * ks + 1], a);
+#pragma unroll
+                for (int np = 0; np < 4; ++np)
+                    product_cols<NP, NP, NI, CH>(m + 2 * np, a, base + Sm::oK, Sm::kTile, np * 16,
+                                                 (k0 >> 3) + 2 * ks, lane);
+            }
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+                to[(part * 8 + nt) * 32 + lane] =
+                    make_float4(m[nt][0], m[nt][1], m[nt][2], m[nt][3]);
+        };
+        if constexpr (!STATES) {
+            by_state(exo);
+            __syncthreads();        // Q has been read
+            copy_bytes(base + Sm::oK, ws.planes(b * in.Hk + hk, c), NI * Sm::kTile, tid, THREADS);
+            cp_commit();
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+                if (nt / (8 / KS) == part) sum_parts<KS>(O[nt], exo, nt, lane);
+            cp_wait<0>();
+            __syncthreads();        // K and L have landed
         }
+        by_state(ex);
+        cp_wait<0>();
+        __syncthreads();
 #pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks) {
-            uint32_t a[NP][4];
-            split_tiles<NP>(S[2 * ks], S[2 * ks + 1], a);
-            const int piece = (k0 >> 3) + 2 * ks;
-#pragma unroll
-            for (int np = 0; np < 4; ++np) {
-                product_cols<NP, NP, NI, CH>(m + 2 * np, a, st + Sm::oK, Sm::kTile, np * 16,
-                                             piece, lane);
-                if constexpr (!STATES)
-                    product_cols<NP, NP, NI, CH>(q + 2 * np, a, st + Sm::oQ, Sm::kTile,
-                                                 np * 16, piece, lane);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                M[i][e] = m[i][e];
-                O[i][e] = q[i][e];
-            }
-        if constexpr (KS > 1) {
-            float4* ex = reinterpret_cast<float4*>(smem + Sm::oExchange) + slice * KS * 256;
-            float4* exo = ex + KS * SL * 256;
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                ex[(part * 8 + nt) * 32 + lane] = make_float4(M[nt][0], M[nt][1], M[nt][2], M[nt][3]);
-                if constexpr (!STATES)
-                    exo[(part * 8 + nt) * 32 + lane] =
-                        make_float4(O[nt][0], O[nt][1], O[nt][2], O[nt][3]);
-            }
-            group_sync(1 + slice, 32 * KS);
-            // every warp adds the parts in the same order
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                sum_parts<KS>(M[nt], ex, nt, lane);
-                if constexpr (!STATES)
-                    if (nt / (8 / KS) == part) sum_parts<KS>(O[nt], exo, nt, lane);
-            }
-        }
+        for (int nt = 0; nt < 8; ++nt) sum_parts<KS>(M[nt], ex, nt, lane);
 
         // Y = V - gamma o (Kh S0), X = B Y (split), Z = Y - L X
         uint32_t x[4][NP][4];
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
             float V[2][4];
-            load_v<SL>(V, smem + stage * Sm::kStage + Sm::oV, np * 16, slice, lane);
+            load_v(V, smem + Sm::oV, np * 16, lane);
             float X[2][4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -429,15 +434,18 @@ delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) 
             C[1].zero();
 #pragma unroll
             for (int jp = 0; jp <= ip; ++jp)
-                product_cols<NP, NP, NP, 8>(C, x[jp], st + Sm::oL, Sm::kLP, ip * 16, 2 * jp, lane);
+                product_cols<NP, NP, NP, 8>(C, x[jp], base + Sm::oL, Sm::kLP, ip * 16, 2 * jp, lane);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) M[2 * ip + j][e] -= C[j][e];
         }
         if constexpr (STATES) {
-            if (live && part == 0)
-                store_rows<NP>(ws.Z(head, c), M, smem + Sm::oOut + warp * kChunk * 32, v0, DP, lane);
+            if (part == 0) store_rows<NP>(ws.Z(head, c), M, smem + Sm::oOut, v0, DP, lane);
+        } else {
+            __syncthreads();        // L has been read
+            copy_bytes(base + Sm::oL, ws.P(head, c), NP * Sm::kLP, tid, THREADS);
+            cp_commit();
         }
 
         // U = B Z; W = exp(G_63 - G) o U for the update
@@ -471,7 +479,7 @@ delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) 
             C[1].zero();
 #pragma unroll
             for (int ts = 0; ts < 4; ++ts)
-                product_rows<NP, NP, NI, CH>(C, w[ts], st + Sm::oK, Sm::kTile, ts * 16,
+                product_rows<NP, NP, NI, CH>(C, w[ts], base + Sm::oK, Sm::kTile, ts * 16,
                                              (k0 >> 3) + 2 * np, lane);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -479,6 +487,10 @@ delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) 
                 S[2 * np + 1][e] = gc * S[2 * np + 1][e] + C[1][e];
             }
         }
+
+        cp_wait<0>();
+        __syncthreads();            // K and V have been read, P has landed
+        if (c + 1 < nc) load(c + 1);
 
         // O^T = gamma o (Qh S0)^T + U^T P^T, this warp's tokens
         if constexpr (!STATES) {
@@ -490,7 +502,7 @@ delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) 
                 C[1].zero();
 #pragma unroll
                 for (int jp = 0; jp <= ip; ++jp)
-                    product_cols<NP, NP, NP, 8>(C, u[jp], st + Sm::oP, Sm::kLP, ip * 16, 2 * jp,
+                    product_cols<NP, NP, NP, 8>(C, u[jp], base + Sm::oL, Sm::kLP, ip * 16, 2 * jp,
                                                 lane);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -501,14 +513,11 @@ delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) 
                         O[nt][e] = in.q_scale * ((e & 1) ? ga.y : ga.x) * O[nt][e] + C[j][e];
                 }
             }
-            if (live)
-                store_out<KS>(o, os.at(b, h, c * kChunk), os.t, O, part, v0, len - c * kChunk, lane);
+            store_out<KS>(o, os.at(b, h, c * kChunk), os.t, O, part, v0, len - c * kChunk, lane);
         }
     }
-    if constexpr (STATES) {
-        if (live) store_image<NP>(ws.states(head, nc), S, v0, k0, DP, D, lane);
-    }
-    if (state_out && live) {
+    if constexpr (STATES) store_image<NP>(ws.states(head, nc), S, v0, k0, DP, D, lane);
+    if (state_out) {
         float* s_out = state_out + (size_t)head * D * D;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -522,7 +531,7 @@ delta_chain_kernel(la_delta in, DeltaWs ws, void* o, Row3 os, float* state_out) 
 
 template <int DP>
 cudaError_t prep(const la_delta& in, const DeltaWs& ws, cudaStream_t st) {
-    using Sm = PrepSmem<DP>;
+    using Sm = PrepSmem;
     const int chunks = (in.T + kChunk - 1) / kChunk;
     auto* kernel = delta_prep_kernel<DP>;
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), Sm::kBytes);
@@ -531,34 +540,28 @@ cudaError_t prep(const la_delta& in, const DeltaWs& ws, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <int DP, int KS, int SL, bool STATES>
+template <int DP, int KS, bool STATES>
 cudaError_t chain(const la_delta& in, const DeltaWs& ws, void* o, Row3 os, float* state_out,
                   cudaStream_t st) {
-    // two stages where they fit (float32 planes of a 128-row state do not)
-    constexpr int STAGES = ChainSmem<DP, KS, SL, 2, STATES>::kBytes <= 227 * 1024 ? 2 : 1;
-    using Sm = ChainSmem<DP, KS, SL, STAGES, STATES>;
-    static_assert(Sm::kBytes <= 227 * 1024, "shared memory of a block");
-    auto* kernel = delta_chain_kernel<DP, KS, SL, STAGES, STATES>;
+    using Sm = ChainSmem<DP, KS, STATES>;
+    auto* kernel = delta_chain_kernel<DP, KS, STATES>;
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), Sm::kBytes);
     if (e != cudaSuccess) return e;
-    const dim3 grid(in.B * in.Hv, (in.D + 16 * SL - 1) / (16 * SL));
-    kernel<<<grid, 32 * KS * SL, Sm::kBytes, st>>>(in, ws, o, os, state_out);
+    kernel<<<dim3(in.B * in.Hv, in.D / 16), 32 * KS, Sm::kBytes, st>>>(in, ws, o, os, state_out);
     return cudaGetLastError();
 }
 
-// A slice of 16 value columns a block (two, which share the chunk's tiles: 368 us
-// beside 295 for 40 heads of 112 with 1000 tokens).
 template <int DP>
 cudaError_t forward(const la_delta& in, const DeltaWs& ws, void* o, Row3 os, float* state_out,
                     cudaStream_t st) {
     const cudaError_t e = prep<DP>(in, ws, st);
-    return e != cudaSuccess ? e : chain<DP, 4, 1, false>(in, ws, o, os, state_out, st);
+    return e != cudaSuccess ? e : chain<DP, 4, false>(in, ws, o, os, state_out, st);
 }
 
 template <int DP>
 cudaError_t states(const la_delta& in, const DeltaWs& ws, cudaStream_t st) {
     const cudaError_t e = prep<DP>(in, ws, st);
-    return e != cudaSuccess ? e : chain<DP, 4, 1, true>(in, ws, nullptr, Row3{0, 0, 0}, nullptr, st);
+    return e != cudaSuccess ? e : chain<DP, 4, true>(in, ws, nullptr, Row3{0, 0, 0}, nullptr, st);
 }
 
 }  // namespace

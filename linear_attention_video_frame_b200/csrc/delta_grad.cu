@@ -25,39 +25,34 @@ namespace {
 // ---------------------------------------------------------------------------
 // The columns of dS evolve independently as those of S do, and the kernel is
 // the forward chain's mirror: a warp holds dS^T of 16 value columns and DP / KS
-// key rows; dO takes v's place.
-template <int DP, int KS, int SL, int STAGES>
+// key rows; dO takes v's place.  K, Q and again K come to one place, P and L to
+// another, so that two blocks share an SM.
+template <int DP, int KS>
 struct ReverseSmem {
     static constexpr int kTile = kChunk * DP * 2;
     static constexpr int kLP = kChunk * kChunk * 2;
-    static constexpr int kV = ValueTile<SL>::kBytes;
     static constexpr int kGates = 3 * kChunk * 4;
-    static constexpr int oK = 0, oQ = oK + kPlanes * kTile, oL = oQ + kPlanes * kTile,
-                         oP = oL + kPlanes * kLP, oV = oP + kPlanes * kLP, oGates = oV + kV,
-                         kStage = oGates + kGates;
-    static constexpr int oExchange = STAGES * kStage;
-    static constexpr int kExchange = KS * SL * 8 * 512;
-    static constexpr int oOut = oExchange + kExchange;
-    static constexpr int kBytes = oOut + SL * kChunk * 32;
+    static constexpr int oK = 0, oP = oK + kPlanes * kTile, oV = oP + kPlanes * kLP,
+                         oGates = oV + ValueTile::kBytes, oExchange = oGates + kGates,
+                         oOut = oExchange + KS * 8 * 512, kBytes = oOut + kChunk * 32;
+    static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two blocks on an SM");
 };
 
-template <int DP, int KS, int SL, int STAGES>
-__global__ void __launch_bounds__(32 * KS * SL)
+template <int DP, int KS>
+__global__ void __launch_bounds__(32 * KS, 2)
 delta_reverse_kernel(la_delta in, DeltaGrad grad, DeltaWs ws) {
-    using Sm = ReverseSmem<DP, KS, SL, STAGES>;
-    constexpr int THREADS = 32 * KS * SL;
+    using Sm = ReverseSmem<DP, KS>;
+    constexpr int THREADS = 32 * KS;
     constexpr int CH = DP / 8, DK = DP / KS, NT = DK / 8;
     constexpr int NP = kPlanes, NI = kPlanes;
     extern __shared__ __align__(128) unsigned char smem[];
     const uint32_t base = smem_u32(smem);
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int slice = warp / KS, part = warp % KS;
+    const int tid = threadIdx.x, lane = tid & 31, part = tid >> 5;
     const int g = lane >> 2, tq = lane & 3;
     const int head = blockIdx.x, b = head / in.Hv, h = head % in.Hv, hk = h / (in.Hv / in.Hk);
     const int D = in.D;
-    const int vb = blockIdx.y * SL * 16, v0 = vb + slice * 16;
-    const bool live = v0 < D;
+    const int v0 = blockIdx.y * 16;
     const int k0 = part * DK;
     const int len = seq_len(in.lengths, b, in.T);
     const int nc = (len + kChunk - 1) / kChunk;
@@ -70,40 +65,28 @@ delta_reverse_kernel(la_delta in, DeltaGrad grad, DeltaWs ws) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int dk = k0 + nt * 8 + 2 * tq + (e & 1), v = v0 + g + 8 * (e >> 1);
-                S[nt][e] = s && live && dk < D ? s[(size_t)dk * D + v] : 0.f;
+                S[nt][e] = s && dk < D ? s[(size_t)dk * D + v] : 0.f;
             }
     }
 
-    auto load = [&](int c, int stage) {
-        const uint32_t st = base + stage * Sm::kStage;
-        const int t0 = c * kChunk;
-        // the planes of K, then of Q
-        copy_bytes(st + Sm::oK, ws.planes(b * in.Hk + hk, c), 2 * NI * Sm::kTile, tid, THREADS);
-        load_values<SL>(st + Sm::oV, grad.d_o, row3(grad.do_stride).at(b, h, 0),
-                             grad.do_stride[2], vb, t0, len, D, tid, THREADS);
-        copy_bytes(st + Sm::oL, ws.L(head, c), NP * Sm::kLP, tid, THREADS);
-        copy_bytes(st + Sm::oP, ws.P(head, c), NP * Sm::kLP, tid, THREADS);
-        copy_bytes(st + Sm::oGates, ws.gates(head, c), Sm::kGates, tid, THREADS);
+    const unsigned char* planes = nullptr;       // of this chunk's K, then of Q
+    auto load_place = [&](int which) {
+        copy_bytes(base + Sm::oK, planes + which * NI * Sm::kTile, NI * Sm::kTile, tid, THREADS);
         cp_commit();
     };
 
-    if (STAGES > 1 && nc > 0) load(nc - 1, 0);
-    for (int i = 0; i < nc; ++i) {
-        const int c = nc - 1 - i;
-        const int stage = STAGES > 1 ? i & 1 : 0;
-        if (STAGES > 1) {
-            cp_wait<0>();
-            __syncthreads();
-            if (c > 0) load(c - 1, stage ^ 1);
-        } else {
-            __syncthreads();
-            load(c, 0);
-            cp_wait<0>();
-            __syncthreads();
-        }
-        const uint32_t st = base + stage * Sm::kStage;
-        const float* gates = reinterpret_cast<const float*>(smem + stage * Sm::kStage + Sm::oGates);
-        if (live) store_image<NP>(ws.dstates(head, c), S, v0, k0, DP, D, lane);
+    for (int c = nc - 1; c >= 0; --c) {
+        planes = ws.planes(b * in.Hk + hk, c);
+        const float* gates = reinterpret_cast<const float*>(smem + Sm::oGates);
+        __syncthreads();            // the chunk behind has been read
+        load_values(base + Sm::oV, grad.d_o, row3(grad.do_stride).at(b, h, 0),
+                       grad.do_stride[2], v0, c * kChunk, len, tid, THREADS);
+        copy_bytes(base + Sm::oP, ws.P(head, c), NP * Sm::kLP, tid, THREADS);
+        copy_bytes(base + Sm::oGates, ws.gates(head, c), Sm::kGates, tid, THREADS);
+        load_place(0);
+        store_image<NP>(ws.dstates(head, c), S, v0, k0, DP, D, lane);
+        cp_wait<0>();
+        __syncthreads();
 
         // (Kh dS)^T, this warp's key rows, then the sum of all
         float M[8][4];
@@ -117,15 +100,16 @@ delta_reverse_kernel(la_delta in, DeltaGrad grad, DeltaWs ws) {
                 split_tiles<NP>(S[2 * ks], S[2 * ks + 1], a);
 #pragma unroll
                 for (int np = 0; np < 4; ++np)
-                    product_cols<NP, NP, NI, CH>(m + 2 * np, a, st + Sm::oK, Sm::kTile, np * 16,
+                    product_cols<NP, NP, NI, CH>(m + 2 * np, a, base + Sm::oK, Sm::kTile, np * 16,
                                                  (k0 >> 3) + 2 * ks, lane);
             }
-            float4* ex = reinterpret_cast<float4*>(smem + Sm::oExchange) + slice * KS * 256;
+            float4* ex = reinterpret_cast<float4*>(smem + Sm::oExchange);
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt)
                 ex[(part * 8 + nt) * 32 + lane] =
                     make_float4(m[nt][0], m[nt][1], m[nt][2], m[nt][3]);
-            group_sync(1 + slice, 32 * KS);
+            __syncthreads();        // K has been read
+            load_place(1);
 #pragma unroll
             for (int nt = 0; nt < 8; ++nt) sum_parts<KS>(M[nt], ex, nt, lane);
         }
@@ -135,7 +119,7 @@ delta_reverse_kernel(la_delta in, DeltaGrad grad, DeltaWs ws) {
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
             float V[2][4], W[2][4];
-            load_v<SL>(V, smem + stage * Sm::kStage + Sm::oV, np * 16, slice, lane);
+            load_v(V, smem + Sm::oV, np * 16, lane);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float2 ga =
@@ -156,7 +140,7 @@ delta_reverse_kernel(la_delta in, DeltaGrad grad, DeltaWs ws) {
             C[1].zero();
 #pragma unroll
             for (int ip = jp; ip < 4; ++ip)
-                product_rows<NP, NI, NP, 8>(C, d[ip], st + Sm::oP, Sm::kLP, ip * 16, 2 * jp, lane);
+                product_rows<NP, NI, NP, 8>(C, d[ip], base + Sm::oP, Sm::kLP, ip * 16, 2 * jp, lane);
             float X[2][4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -173,6 +157,24 @@ delta_reverse_kernel(la_delta in, DeltaGrad grad, DeltaWs ws) {
             }
             split_tiles<NP>(X[0], X[1], x[jp]);
         }
+        cp_wait<0>();
+        __syncthreads();            // Q has landed, P has been read
+        copy_bytes(base + Sm::oP, ws.L(head, c), NP * Sm::kLP, tid, THREADS);
+        cp_commit();
+        // the update's part of Q: (gamma o dO)^T Qh
+        Acc up[NT];
+#pragma unroll
+        for (int np = 0; np < NT / 2; ++np) {
+            up[2 * np].zero();
+            up[2 * np + 1].zero();
+#pragma unroll
+            for (int ts = 0; ts < 4; ++ts)
+                product_rows<NP, NP, NI, CH>(up + 2 * np, gd[ts], base + Sm::oK, Sm::kTile, ts * 16,
+                                             (k0 >> 3) + 2 * np, lane);
+        }
+        cp_wait<0>();
+        __syncthreads();            // L has landed, Q has been read
+        load_place(0);
         // dX = dU - L^T X
 #pragma unroll
         for (int jp = 0; jp < 4; ++jp) {
@@ -181,14 +183,13 @@ delta_reverse_kernel(la_delta in, DeltaGrad grad, DeltaWs ws) {
             C[1].zero();
 #pragma unroll
             for (int ip = jp; ip < 4; ++ip)
-                product_rows<NP, NP, NP, 8>(C, x[ip], st + Sm::oL, Sm::kLP, ip * 16, 2 * jp, lane);
+                product_rows<NP, NP, NP, 8>(C, x[ip], base + Sm::oP, Sm::kLP, ip * 16, 2 * jp, lane);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) M[2 * jp + j][e] -= C[j][e];
         }
-        if (live && part == 0)
-            store_rows<NP>(ws.dX(head, c), M, smem + Sm::oOut + slice * kChunk * 32, v0, DP, lane);
+        if (part == 0) store_rows<NP>(ws.dX(head, c), M, smem + Sm::oOut, v0, DP, lane);
 
         // dS^T <- gamma_63 dS^T + (gamma o dO)^T Qh - (gamma B dX)^T Kh
         uint32_t w[4][NP][4];
@@ -208,18 +209,15 @@ delta_reverse_kernel(la_delta in, DeltaGrad grad, DeltaWs ws) {
             split_tiles<NP>(W[0], W[1], w[np]);
         }
         const float gc = gates[kChunk - 1];
+        cp_wait<0>();
+        __syncthreads();            // K has landed
 #pragma unroll
         for (int np = 0; np < NT / 2; ++np) {
-            Acc C[2];
-            C[0].zero();
-            C[1].zero();
+            Acc* C = up + 2 * np;
 #pragma unroll
-            for (int ts = 0; ts < 4; ++ts) {
-                product_rows<NP, NP, NI, CH>(C, gd[ts], st + Sm::oQ, Sm::kTile, ts * 16,
+            for (int ts = 0; ts < 4; ++ts)
+                product_rows<NP, NP, NI, CH>(C, w[ts], base + Sm::oK, Sm::kTile, ts * 16,
                                              (k0 >> 3) + 2 * np, lane);
-                product_rows<NP, NP, NI, CH>(C, w[ts], st + Sm::oK, Sm::kTile, ts * 16,
-                                             (k0 >> 3) + 2 * np, lane);
-            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 S[2 * np][e] = gc * S[2 * np][e] + C[0][e];
@@ -227,7 +225,7 @@ delta_reverse_kernel(la_delta in, DeltaGrad grad, DeltaWs ws) {
             }
         }
     }
-    if (grad.dstate_in && live) {
+    if (grad.dstate_in) {
         float* s = grad.dstate_in + (size_t)head * D * D;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -672,15 +670,12 @@ delta_grad_kernel(la_delta in, DeltaGrad grad, DeltaWs ws, int chunks) {
 
 template <int DP>
 cudaError_t reverse(const la_delta& in, const DeltaGrad& g, const DeltaWs& ws, cudaStream_t st) {
-    constexpr int KS = 4, SL = 1;
-    constexpr int STAGES = ReverseSmem<DP, KS, SL, 2>::kBytes <= 227 * 1024 ? 2 : 1;
-    using Rs = ReverseSmem<DP, KS, SL, STAGES>;
-    static_assert(Rs::kBytes <= 227 * 1024, "shared memory of a block");
-    auto* kernel = delta_reverse_kernel<DP, KS, SL, STAGES>;
+    constexpr int KS = 4;
+    using Rs = ReverseSmem<DP, KS>;
+    auto* kernel = delta_reverse_kernel<DP, KS>;
     const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(kernel), Rs::kBytes);
     if (e != cudaSuccess) return e;
-    const dim3 grid(in.B * in.Hv, (in.D + 16 * SL - 1) / (16 * SL));
-    kernel<<<grid, 32 * KS * SL, Rs::kBytes, st>>>(in, g, ws);
+    kernel<<<dim3(in.B * in.Hv, in.D / 16), 32 * KS, Rs::kBytes, st>>>(in, g, ws);
     return cudaGetLastError();
 }
 

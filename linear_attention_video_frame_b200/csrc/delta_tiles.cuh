@@ -181,21 +181,8 @@ cudaError_t launch_delta_states(const la_delta& in, const DeltaWs& ws, cudaStrea
 
 #ifdef __CUDACC__
 
-// Rows t0 .. t0 + 63 of a bf16 [T, D] matrix as a tile of DP columns, by
-// asynchronous copies.  Rows from `len` on and columns from D on are 0 and not read.
-template <int DP>
-__device__ __forceinline__ void load_rows(uint32_t dst, const void* src, long long offset,
-                                          long long stride, int t0, int len, int D, int tid,
-                                          int threads) {
-    constexpr int CH = DP / 8;
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(src) + offset;
-    for (int i = tid; i < kChunk * CH; i += threads) {
-        const int r = i / CH, c = i % CH;
-        const bool on = t0 + r < len && c * 8 < D;
-        cp16(dst + tile_at<CH>(r, c), on ? p + (t0 + r) * stride + c * 8 : p, on);
-    }
-}
-// The same of a float32 matrix, split into planes.
+// Rows t0 .. t0 + 63 of a float32 [T, D] matrix as tiles of DP columns, split into
+// planes.  Rows from `len` on and columns from D on are 0 and not read.
 template <int DP>
 __device__ __forceinline__ void load_rows_split(uint32_t dst, const void* src, long long offset,
                                                 long long stride, int t0, int len, int D, int tid,
@@ -334,10 +321,6 @@ __device__ __forceinline__ void chunk_gates(const RawGates& raw, float* gates, f
     }
 }
 
-__device__ __forceinline__ void group_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
-}
-
 template <int KS>
 __device__ __forceinline__ void sum_parts(float (&m)[4], const float4* ex, int nt, int lane) {
     float4 s = ex[nt * 32 + lane];
@@ -349,36 +332,29 @@ __device__ __forceinline__ void sum_parts(float (&m)[4], const float4* ex, int n
     m[0] = s.x; m[1] = s.y; m[2] = s.z; m[3] = s.w;
 }
 
-// The block's value columns vb .. vb + 16 SL - 1 of a chunk's rows, as rows of
-// SL * 16 + 4 floats.  0 where there is none.
-template <int SL>
+// Value columns v0 .. v0 + 15 of a chunk's rows, as rows of 20 floats.  0 behind `len`.
 struct ValueTile {
-    static constexpr int kPitch = SL * 16 + 4;
-    static constexpr int kBytes = kChunk * kPitch * 4;
+    static constexpr int kPitch = 20, kBytes = kChunk * kPitch * 4;
 };
-template <int SL>
 __device__ __forceinline__ void load_values(uint32_t dst, const void* src, long long offset,
-                                            long long stride, int vb, int t0, int len, int D,
-                                            int tid, int threads) {
-    constexpr int CH = SL * 4;
-    for (int i = tid; i < kChunk * CH; i += threads) {
-        const int r = i / CH, c = i % CH;
-        const bool on = t0 + r < len && vb + c * 4 < D;
-        cp16(dst + (r * ValueTile<SL>::kPitch + c * 4) * 4,
-             static_cast<const float*>(src) + (on ? offset + (t0 + r) * stride + vb + c * 4 : 0), on);
+                                            long long stride, int v0, int t0, int len, int tid,
+                                            int threads) {
+    for (int i = tid; i < kChunk * 4; i += threads) {
+        const int r = i >> 2, c = i & 3;
+        const bool on = t0 + r < len;
+        cp16(dst + (r * ValueTile::kPitch + c * 4) * 4,
+             static_cast<const float*>(src) + (on ? offset + (t0 + r) * stride + v0 + c * 4 : 0), on);
     }
 }
 
-// 16 tokens of a slice's 16 value columns, transposed into two product tiles.
-template <int SL>
-__device__ __forceinline__ void load_v(float (&V)[2][4], const unsigned char* ptr, int row,
-                                       int slice, int lane) {
-    const float* v = reinterpret_cast<const float*>(ptr) + slice * 16 + (lane >> 2);
+// 16 tokens of it, transposed into two product tiles.
+__device__ __forceinline__ void load_v(float (&V)[2][4], const unsigned char* ptr, int row, int lane) {
+    const float* v = reinterpret_cast<const float*>(ptr) + (lane >> 2);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            V[j][e] = v[(row + j * 8 + 2 * (lane & 3) + (e & 1)) * ValueTile<SL>::kPitch + 8 * (e >> 1)];
+            V[j][e] = v[(row + j * 8 + 2 * (lane & 3) + (e & 1)) * ValueTile::kPitch + 8 * (e >> 1)];
 }
 
 // S^T tiles of a warp (16 value columns, key rows from k0) into an image.
