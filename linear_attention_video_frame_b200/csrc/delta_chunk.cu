@@ -566,13 +566,13 @@ cudaError_t states(const la_delta& in, const DeltaWs& ws, cudaStream_t st) {
 
 }  // namespace
 
-// From how many tokens on a call goes by chunks.  One chunk costs 21 to 28 us (bf16)
-// or 25 to 36 (float32, 95 with 160 heads of 128) however few of its tokens there are;
-// token by token costs 1 us each, 2.7 with 160 heads of 128.
+// From how many tokens on a call goes by chunks.  One chunk costs 20 to 27 us (bf16)
+// or 23 to 33 (float32), with 160 heads of 128 37 and 66, however few of its tokens
+// there are; token by token costs 6 us and 0.7 a token, 2.7 with 160 heads of 128.
 bool delta_chunked(int backward, int dt, int heads, int T, int D) {
     if (backward) return true;
     if (D > 128) return false;
-    return T >= (dt == LA_F32 ? 40 : heads >= 64 ? 12 : 24);
+    return T >= (heads >= 64 ? (dt == LA_F32 ? 24 : 16) : dt == LA_F32 ? 40 : 24);
 }
 
 size_t delta_workspace_bytes(int backward, int dt, int B, int Hk, int Hv, int T, int D) {

@@ -12,6 +12,7 @@ contiguous float32; lengths ``[B]`` is int32 or None.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 
 import torch
@@ -94,20 +95,25 @@ def la_norm_workspace_size(rows: int, N: int) -> int:
     return int(lib.la_norm_workspace_size(rows, N))
 
 
-def _here(t: torch.Tensor, name: str) -> torch.device:
+# sizes depend on nothing but their arguments
+_delta_need = functools.lru_cache(maxsize=4096)(lib.la_delta_workspace_size)
+_norm_need = functools.lru_cache(maxsize=4096)(lib.la_norm_workspace_size)
+
+
+def _here(t: torch.Tensor, name: str) -> int:
     """Kernels run on the current device, and the first tensor must live there."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    device = t.device
-    if device.index != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors are on {device}, the current device is "
+    device = t.get_device()
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors are on {t.device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     return device
 
 
-def _raw_stream(stream, device: torch.device):
+def _raw_stream(stream, device: int):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(device)
     return _stream(stream)
 
 
@@ -115,9 +121,10 @@ def _full(t, name: str, shape, dtype, device):
     """The address of a contiguous tensor of this shape, dtype and device; None stays None."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or \
+            not t.is_contiguous():
         _check(t, name, shape, dtype)
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     return t.data_ptr()
 
 
@@ -138,7 +145,7 @@ def _rows(t, name: str, shape, dtype, device):
     """The strides of [..., D] rows, which are contiguous themselves.  The stride of an axis of
     one element is never taken; torch may report any value for it."""
     s = t.stride()
-    if t.shape != shape or t.dtype is not dtype or t.device != device or \
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or \
             (s[-1] != 1 and shape[-1] != 1):
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
@@ -146,8 +153,8 @@ def _rows(t, name: str, shape, dtype, device):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if t.dtype is not dtype:
             raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
         raise ValueError(f"the rows of {name} must be contiguous")
     if len(shape) == 3:             # one token
         return (s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0, 0)
@@ -197,7 +204,7 @@ def la_gated_delta_rule(q, k, v, log_alpha, beta, k_scale: float = 1.0, q_scale:
         o = _new_rows(v, lengths)
     os = _rows(o, "o", (B, Hv, T, D), q.dtype, device)
     end = _full(state_out, "state_out", (B, Hv, D, D), torch.float32, device)
-    need = lib.la_delta_workspace_size(0, code, B, q.shape[1], Hv, T, D)
+    need = _delta_need(0, code, B, q.shape[1], Hv, T, D)
     if need == 0:
         raise LaScanError(LA_ERR_UNSUPPORTED, "la_gated_delta_rule")
     workspace = _space(workspace, need, q, stream)
@@ -253,7 +260,7 @@ def la_gated_delta_rule_backward(q, k, v, log_alpha, beta, do, k_scale: float = 
 
     dq, dk, dv = out(dq, kshape, dtype), out(dk, kshape, dtype), out(dv, vshape, dtype)
     dlog_alpha, dbeta = out(dlog_alpha, vshape[:3], f32), out(dbeta, vshape[:3], f32)
-    need = lib.la_delta_workspace_size(1, code, B, kshape[1], Hv, T, D)
+    need = _delta_need(1, code, B, kshape[1], Hv, T, D)
     if need == 0:
         raise LaScanError(LA_ERR_UNSUPPORTED, "la_gated_delta_rule_backward")
     workspace = _space(workspace, need, q, stream)
@@ -334,7 +341,7 @@ def la_add_rms_norm_backward(dy, h, weight, dh=None, eps: float = 1e-6, dx=None,
         if dweight is None:
             dweight = torch.empty_like(weight)
         pdw = _full(dweight, "dweight", (N,), torch.float32, device)
-        workspace = _space(workspace, lib.la_norm_workspace_size(rows, N), h, stream)
+        workspace = _space(workspace, _norm_need(rows, N), h, stream)
         space, size = workspace.data_ptr(), workspace.numel()
     else:
         dweight = None

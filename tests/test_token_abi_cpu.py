@@ -90,7 +90,8 @@ def test_step_and_backward_refusals():
 
 
 def test_delta_sizes_and_plans():
-    for dt, heads, first in ((la.LA_BF16, 1, 24), (la.LA_BF16, 64, 12), (la.LA_F32, 64, 40)):
+    for dt, heads, first in ((la.LA_BF16, 1, 24), (la.LA_BF16, 64, 16), (la.LA_F32, 1, 40),
+                             (la.LA_F32, 64, 24)):
         assert la.la_delta_plan(False, dt, 1, 1, heads, first - 1, 64) == ("delta_recurrent", 1)
         assert la.la_delta_plan(False, dt, 1, 1, heads, first, 64) == ("delta_chunked", 2)
     assert la.la_delta_plan(False, la.LA_F32, 1, 1, 1, 64, 144)[0] == "delta_recurrent"
