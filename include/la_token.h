@@ -70,7 +70,7 @@ typedef struct la_delta {
  * workspace: la_delta_workspace_size(0, ...) bytes, 256-byte aligned.
  *
  * Heads up to 128 wide run chunked on tensor cores (chunks of 64 tokens) from about
- * 12 to 40 tokens on, by type and number of heads; shorter calls and wider heads run
+ * 16 to 40 tokens on, by type and number of heads; shorter calls and wider heads run
  * token by token in float32 (la_delta_plan tells).  With few heads a long sequence is
  * cut into segments that run side by side.
  * The chunked kernels bound every wait on the device; la_query_device_status(workspace,

@@ -11,7 +11,7 @@
 // One token is bound by the state's traffic (8 D^2 bytes a head).  A block of
 // 256 threads holds 16 KB of a 128-row state: 8 threads side by side take one
 // 128-byte row piece, so every access is a full line, and each thread has its
-// four 16-byte loads in flight at once.  192 x 32 heads of 128: 151 us, 5.3 TB/s
+// four 16-byte loads in flight at once.  192 x 32 heads of 128: 156 us, 5.2 TB/s
 // (with k and q in registers and three blocks an SM 187 us).
 #include <cuda_bf16.h>
 

@@ -9,6 +9,10 @@
 // X L^T with Z = Y - X L^T for the backward pass.  Each of the 16 compute warps
 // owns 32 value columns (its quarter of the lanes) and a quarter of the tokens
 // (16) and of the key rows.  Three load warps keep the next chunk in flight.
+//
+// The chain of products and register work bounds it, not its bytes: 2300 cycles of
+// products and as many of register work depend on one another, 3.3 to 3.8 us a chunk
+// in all (80 heads of 128, 32 chunks: 118 us, DRAM at 24 % of its peak).
 #include "delta_tc.cuh"
 
 namespace la {

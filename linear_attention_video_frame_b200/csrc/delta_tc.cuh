@@ -132,7 +132,8 @@ __device__ __forceinline__ void arrive(uint64_t* bar, int lane) {
 }
 
 // One warp's copy of ROWS (64) rows of a [T, D] matrix as 128-byte swizzled
-// blocks of 64 columns, `half` bytes apart.  Rows behind the sequence are 0 and not read; columns behind D are left alone.
+// blocks of 64 columns, `half` bytes apart.  Rows behind the sequence are 0 and not
+// read; columns behind D are left alone.
 // A lane keeps to one 16-byte column, so that a copy costs three instructions
 // (row and column taken from a running index cost 6000 cycles a chunk).
 template <int ROWS = kChunk>

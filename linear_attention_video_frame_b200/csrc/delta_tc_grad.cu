@@ -20,7 +20,8 @@ constexpr int kGradWarps = 8, kGradThreads = kGradWarps * 32;
 // Value columns go 64 at a time, so that two blocks fit an SM: a block is a
 // sequence of loads, conversions and products that wait for one another, and the
 // second block fills its waits (one block of 16 warps with all columns at once:
-// 317 us for 2048 chunks of 128, most of it waiting).
+// 317 us for 2048 chunks of 128, most of it waiting; as it is 212, DRAM at 36 % of its
+// peak).
 template <int DP>
 struct GradTc {
     static constexpr int kHalves = DP / 64;                 // of the key rows

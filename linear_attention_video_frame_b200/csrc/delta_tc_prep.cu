@@ -13,8 +13,9 @@
 // that the tiles of one product are the a operand of the next.  L: the diagonal
 // blocks by forward substitution (a column a lane), then
 //     R = N_rc - sum_j N_rj (B L_jc),   L_rc = R - L_rr (B R).
-// A block is one chunk's sequence of such steps, bound by their latency: four blocks
-// share an SM.
+// A block is one chunk's sequence of such steps, bound by their latency (27,000 cycles,
+// of which the products take 2,000): four blocks share an SM.  2560 chunks of 128:
+// 67 us, DRAM at 22 % of its peak; with K K^T, Q K^T and Kt on warp-level products 86.
 #include "delta_tc.cuh"
 
 namespace la {

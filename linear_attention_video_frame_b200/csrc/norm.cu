@@ -5,7 +5,8 @@
 // sums are taken there in float32, and the results leave once.  A thread
 // holds VPT vectors of 8 neighbouring columns (16 bytes of bf16); 16
 // neighbouring lanes then hold the 128 columns of one scale group, so a
-// group's maximum takes four shuffles and no shared memory.
+// group's maximum takes four shuffles and no shared memory.  28160 rows of 2560 in
+// bf16 with a residual: 90 us, 5.6 TB/s; backward, 8192 rows of 2560: 45 us, 3.7 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -318,7 +319,7 @@ norm_fp8_kernel(const T* x, const T* residual, const float* weight, T* h, uint8_
 // come next are on their way to shared memory, each thread's own pieces, so that no
 // barrier but the sums' is needed; they are read again after it, so that the
 // registers in between are free for more blocks.  (Kept in registers, three blocks an
-// SM: 57 us for 8192 rows of 2560 in bf16, beside 47.)
+// SM: 57 us for 8192 rows of 2560 in bf16, beside 45.)
 constexpr int kNormStages = 2;
 template <typename T, int VPT, bool STAGES>
 __global__ void __launch_bounds__(512, STAGES && sizeof(T) == 2 ? 2 : 1)
