@@ -351,3 +351,15 @@ def test_other_stream_without_a_workspace():
                        dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     assert _same(o, want[0]) and _same(end, want[1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,D", [(0, 64), (1, 64), (200, 64), (200, 128), (3, 144)])
+def test_status_of_a_call(T, D, dtype):
+    """Every call leaves its status in its workspace, whatever was there."""
+    x = delta_inputs(1, 2, 2, T, D, dtype, seed=60 + T)
+    code = la.LA_BF16 if dtype == BF16 else la.LA_F32
+    for backward in (False, True)[:1 if D > 128 else 2]:
+        ws = la.delta_workspace_for(backward, code, 1, 2, 2, T, D).fill_(255)
+        (_backward if backward else _forward)(x, workspace=ws)
+        assert la.la_query_device_status(ws) == la.LA_OK
