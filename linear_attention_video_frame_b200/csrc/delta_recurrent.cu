@@ -8,11 +8,13 @@
 // so the state is read once, both products share that read, and the output
 // needs no second pass over the updated state.
 //
-// One token is bound by the state's traffic (8 D^2 bytes a head).  A block of
-// 256 threads holds 16 KB of a 128-row state: 8 threads side by side take one
-// 128-byte row piece, so every access is a full line, and each thread has its
-// four 16-byte loads in flight at once.  192 x 32 heads of 128: 156 us, 5.2 TB/s
-// (with k and q in registers and three blocks an SM 187 us).
+// One token is bound by the state's traffic (8 D^2 bytes a head).  A block of 128
+// threads holds 16 KB of a 128-row state: 8 threads side by side take one 128-byte
+// row piece, so every access is a full line, each thread has its eight 16-byte loads
+// in flight at once, and few warps wait for one another at a block's two barriers.
+// 192 x 32 heads of 128: 130 us, 6.2 TB/s (256 threads of four loads: 157).  Eight
+// blocks an SM, which leaves a thread 64 registers; with six of 80 heads of 112 and 256
+// take a tenth longer.
 #include <cuda_bf16.h>
 
 #include "token.cuh"
@@ -142,22 +144,22 @@ delta_recurrent_kernel(la_delta in, T* o, Row3 os, float* state_out, unsigned in
 }
 
 // One token.  All of a block's state is asked for before anything else; k and q
-// come through shared memory, so that a thread holds little beside its 16 state
-// values and five blocks (80 KB of loads) are in flight on an SM.
-template <typename T, int ROWS>
-__global__ void __launch_bounds__(kThreads, ROWS > 4 ? 3 : 5)
+// come through shared memory, so that a thread holds little beside its state.
+template <typename T, int THREADS, int COLS, int ROWS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 delta_step_kernel(la_delta in, T* o, Row3 os, float* state_out, unsigned int* status) {
     if (status && blockIdx.x + blockIdx.y + blockIdx.z == 0 && threadIdx.x < 2) status[threadIdx.x] = 0;
-    __shared__ float4 part[kThreads / 32][kCols / 4][2];
-    __shared__ float dots[kThreads / 32];
-    __shared__ float2 kq[ROWS * kRowGroups];
+    constexpr int CG = COLS / 4, RG = THREADS / CG;      // threads side by side, below
+    __shared__ float4 part[THREADS / 32][CG][2];
+    __shared__ float dots[THREADS / 32];
+    __shared__ float2 kq[ROWS * RG];
 
     const int h = blockIdx.y, b = blockIdx.z;
     const int hk = h / (in.Hv / in.Hk);
     const int D = in.D;
-    const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3;
+    const int cg = threadIdx.x % CG, rg = threadIdx.x / CG;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int col = blockIdx.x * kCols + cg * 4;
+    const int col = blockIdx.x * COLS + cg * 4;
     const bool live = col < D;
     const size_t head = (size_t)b * in.Hv + h;
     const bool on = seq_len(in.lengths, b, 1) > 0;
@@ -167,7 +169,7 @@ delta_step_kernel(la_delta in, T* o, Row3 os, float* state_out, unsigned int* st
     float4 S[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-        const int r = rg + i * kRowGroups;
+        const int r = rg + i * RG;
         S[i] = (s_in && live && r < D)
                    ? __ldcs(reinterpret_cast<const float4*>(s_in + (size_t)r * D + col))
                    : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -177,7 +179,7 @@ delta_step_kernel(la_delta in, T* o, Row3 os, float* state_out, unsigned int* st
         const T* k = static_cast<const T*>(in.k) + row3(in.k_stride).at(b, hk, 0);
         const T* v = static_cast<const T*>(in.v) + row3(in.v_stride).at(b, h, 0);
         const float alpha = expf(in.log_alpha[head]), beta = in.beta[head];
-        if (threadIdx.x < ROWS * kRowGroups)
+        if (threadIdx.x < ROWS * RG)
             kq[threadIdx.x] = threadIdx.x < D ? make_float2(ld(k + threadIdx.x) * in.k_scale,
                                                             ld(q + threadIdx.x) * in.q_scale)
                                               : make_float2(0.f, 0.f);
@@ -189,23 +191,23 @@ delta_step_kernel(la_delta in, T* o, Row3 os, float* state_out, unsigned int* st
         float qk = 0.f;
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            const float2 f = kq[rg + i * kRowGroups];
+            const float2 f = kq[rg + i * RG];
             m.x += f.x * S[i].x; m.y += f.x * S[i].y;
             m.z += f.x * S[i].z; m.w += f.x * S[i].w;
             p.x += f.y * S[i].x; p.y += f.y * S[i].y;
             p.z += f.y * S[i].z; p.w += f.y * S[i].w;
             qk += f.x * f.y;
         }
-        // the four rows of a warp that share a column group
+        // the rows of a warp that share a column group
 #pragma unroll
-        for (int d = 8; d < 32; d <<= 1) {
+        for (int d = CG; d < 32; d <<= 1) {
             m.x += __shfl_xor_sync(~0u, m.x, d); m.y += __shfl_xor_sync(~0u, m.y, d);
             m.z += __shfl_xor_sync(~0u, m.z, d); m.w += __shfl_xor_sync(~0u, m.w, d);
             p.x += __shfl_xor_sync(~0u, p.x, d); p.y += __shfl_xor_sync(~0u, p.y, d);
             p.z += __shfl_xor_sync(~0u, p.z, d); p.w += __shfl_xor_sync(~0u, p.w, d);
             qk += __shfl_xor_sync(~0u, qk, d);
         }
-        if (lane < 8) {
+        if (lane < CG) {
             part[warp][cg][0] = m;
             part[warp][cg][1] = p;
             if (lane == 0) dots[warp] = qk;
@@ -214,7 +216,7 @@ delta_step_kernel(la_delta in, T* o, Row3 os, float* state_out, unsigned int* st
         m = p = make_float4(0.f, 0.f, 0.f, 0.f);
         qk = 0.f;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
+        for (int w = 0; w < THREADS / 32; ++w) {
             const float4 a = part[w][cg][0];
             m.x += a.x; m.y += a.y; m.z += a.z; m.w += a.w;
         }
@@ -222,7 +224,7 @@ delta_step_kernel(la_delta in, T* o, Row3 os, float* state_out, unsigned int* st
                                      beta * (vv[2] - alpha * m.z), beta * (vv[3] - alpha * m.w));
         if (rg == 0 && live) {
 #pragma unroll
-            for (int w = 0; w < kThreads / 32; ++w) {
+            for (int w = 0; w < THREADS / 32; ++w) {
                 const float4 c = part[w][cg][1];
                 p.x += c.x; p.y += c.y; p.z += c.z; p.w += c.w;
                 qk += dots[w];
@@ -235,7 +237,7 @@ delta_step_kernel(la_delta in, T* o, Row3 os, float* state_out, unsigned int* st
         }
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            const float f = kq[rg + i * kRowGroups].x;
+            const float f = kq[rg + i * RG].x;
             S[i].x = alpha * S[i].x + f * u.x; S[i].y = alpha * S[i].y + f * u.y;
             S[i].z = alpha * S[i].z + f * u.z; S[i].w = alpha * S[i].w + f * u.w;
         }
@@ -244,7 +246,7 @@ delta_step_kernel(la_delta in, T* o, Row3 os, float* state_out, unsigned int* st
     float* s_out = state_out + head * D * D;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-        const int r = rg + i * kRowGroups;
+        const int r = rg + i * RG;
         if (live && r < D) __stcs(reinterpret_cast<float4*>(s_out + (size_t)r * D + col), S[i]);
     }
 }
@@ -252,16 +254,17 @@ delta_step_kernel(la_delta in, T* o, Row3 os, float* state_out, unsigned int* st
 template <typename T>
 void launch_typed(const la_delta& in, void* o, const long long os[3], float* state_out,
                   unsigned int* status, cudaStream_t st) {
-    const dim3 grid((in.D + kCols - 1) / kCols, in.Hv, in.B);
+    auto grid_of = [&](int cols) { return dim3((in.D + cols - 1) / cols, in.Hv, in.B); };
+    const dim3 grid = grid_of(kCols);
     T* out = static_cast<T*>(o);
     const Row3 r = o ? row3(os) : Row3{0, 0, 0};
     if (in.T == 1) {
         if (in.D <= 64)
-            delta_step_kernel<T, 2><<<grid, kThreads, 0, st>>>(in, out, r, state_out, status);
+            delta_step_kernel<T, 128, 64, 8><<<grid_of(64), 128, 0, st>>>(in, out, r, state_out, status);
         else if (in.D <= 128)
-            delta_step_kernel<T, 4><<<grid, kThreads, 0, st>>>(in, out, r, state_out, status);
+            delta_step_kernel<T, 128, 32, 8><<<grid, 128, 0, st>>>(in, out, r, state_out, status);
         else
-            delta_step_kernel<T, 8><<<grid, kThreads, 0, st>>>(in, out, r, state_out, status);
+            delta_step_kernel<T, 256, 32, 8><<<grid, 256, 0, st>>>(in, out, r, state_out, status);
         return;
     }
     if (in.D <= 64)

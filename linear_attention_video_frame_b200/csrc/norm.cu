@@ -447,23 +447,29 @@ norm_backward_kernel(const T* dy, const T* h, const float* weight, const T* dh, 
     }
 }
 
-// dweight = sum of the blocks' partial sums: 32 columns a block, 32 threads
+// dweight = sum of the blocks' partial sums: COLS columns a block, 1024 / COLS threads
 // down the partials of a column, joined in a fixed order.
+template <int COLS>
 __global__ void __launch_bounds__(1024)
 norm_dweight_kernel(const float* partial, float* dweight, int blocks, int N) {
+    constexpr int DOWN = 1024 / COLS;
     __shared__ float sum[32][33];
-    const int c = blockIdx.x * 32 + threadIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x * COLS + threadIdx.x % COLS;
     float s = 0.f;
     if (c < N)
 #pragma unroll 8
-        for (int i = threadIdx.y; i < blocks; i += 32) s += partial[(size_t)i * N + c];
-    sum[threadIdx.y][threadIdx.x] = s;
+        for (int i = threadIdx.x / COLS; i < blocks; i += DOWN) s += partial[(size_t)i * N + c];
+#pragma unroll
+    for (int d = COLS; d < 32; d <<= 1) s += __shfl_xor_sync(~0u, s, d);
+    if (lane < COLS) sum[warp][lane] = s;
     __syncthreads();
-    float t = sum[threadIdx.x][threadIdx.y];
+    if (warp >= COLS) return;
+    float t = sum[lane][warp];
 #pragma unroll
     for (int d = 16; d; d >>= 1) t += __shfl_xor_sync(~0u, t, d);
-    const int out = blockIdx.x * 32 + threadIdx.y;
-    if (threadIdx.x == 0 && out < N) dweight[out] = t;
+    const int out = blockIdx.x * COLS + warp;
+    if (lane == 0 && out < N) dweight[out] = t;
 }
 
 // Vectors a thread holds, and the threads of a row (at most 512 for N <= 16384).
@@ -560,8 +566,12 @@ cudaError_t launch_norm_backward(const void* dy, const void* h, const float* wei
                                    : pick(static_cast<float*>(nullptr));
         if (e != cudaSuccess) return e;
     }
-    if (dweight)
-        norm_dweight_kernel<<<(N + 31) / 32, dim3(32, 32), 0, st>>>(partial, dweight, blocks, N);
+    // Few columns leave most SMs without a block: 8 columns a block take 8 us for N = 256
+    // (32 a block 12), but 10 for N = 2560, whose rows are read by sectors then (6).
+    if (dweight && N < 1024)
+        norm_dweight_kernel<8><<<N / 8, 1024, 0, st>>>(partial, dweight, blocks, N);
+    else if (dweight)
+        norm_dweight_kernel<32><<<(N + 31) / 32, 1024, 0, st>>>(partial, dweight, blocks, N);
     return cudaGetLastError();
 }
 
