@@ -6,7 +6,7 @@
 // holds VPT vectors of 8 neighbouring columns (16 bytes of bf16); 16
 // neighbouring lanes then hold the 128 columns of one scale group, so a
 // group's maximum takes four shuffles and no shared memory.  28160 rows of 2560 in
-// bf16 with a residual: 90 us, 5.6 TB/s; backward, 8192 rows of 2560: 45 us, 3.7 TB/s.
+// bf16 with a residual: 90 us, 5.6 TB/s; backward, 8192 rows of 2560: 37 us, 4.5 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -315,14 +315,16 @@ norm_fp8_kernel(const T* x, const T* residual, const float* weight, T* h, uint8_
 }
 
 // A block takes every gridDim.x-th row and keeps its share of dweight in
-// registers; dweight's partial sums leave once a block.  With STAGES, the rows that
-// come next are on their way to shared memory, each thread's own pieces, so that no
-// barrier but the sums' is needed; they are read again after it, so that the
-// registers in between are free for more blocks.  (Kept in registers, three blocks an
-// SM: 57 us for 8192 rows of 2560 in bf16, beside 45.)
+// registers, with the weight beside it (up to 8192 columns); dweight's partial sums
+// leave once a block.  With STAGES, the rows that come next are on their way to shared
+// memory, each thread's own pieces, so that no barrier but the sums' is needed; they
+// are read again after it, so that a thread needs no more than 96 registers and four
+// blocks of 160 share an SM.  8192 rows of 2560 in bf16: 37 us with dweight's 6 (64
+// registers and six blocks, which read the weight twice a row: 45; rows in registers
+// and three blocks took a fifth longer than that).
 constexpr int kNormStages = 2;
 template <typename T, int VPT, bool STAGES>
-__global__ void __launch_bounds__(512, STAGES && sizeof(T) == 2 ? 2 : 1)
+__global__ void __maxnreg__(VPT > 2 ? 128 : 96)
 norm_backward_kernel(const T* dy, const T* h, const float* weight, const T* dh, T* dx,
                      float* partial, long long rows, int N, float eps) {
     extern __shared__ __align__(16) unsigned char ring[];      // [stage][h, dy, dh][N]
@@ -330,11 +332,22 @@ norm_backward_kernel(const T* dy, const T* h, const float* weight, const T* dh, 
     int buf = 0;
     const int nv = N / 8;
     const int warps = blockDim.x >> 5;
-    Vec8 dw[VPT];
+    constexpr bool KEEP = VPT <= 2;
+    Vec8 dw[VPT], kept[KEEP ? VPT : 1];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i].x[j] = 0.f;
+    if (KEEP)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            if (c < nv) kept[i] = load8(weight + c * 8);
+        }
+    auto weights = [&](int i, int c) -> Vec8 {
+        if constexpr (KEEP) return kept[i];
+        else return load8(weight + c * 8);
+    };
     constexpr int PIECES = sizeof(T) / 2;  // 16-byte pieces of a vector
     auto place = [&](int stage, int which, int c) {
         return ring + ((size_t)(stage * 3 + which) * N + c * 8) * sizeof(T);
@@ -390,7 +403,7 @@ norm_backward_kernel(const T* dy, const T* h, const float* weight, const T* dh, 
             const int c = threadIdx.x + i * blockDim.x;
             if (c >= nv) continue;
             ss += f[i].squares();
-            const Vec8 w = load8(weight + c * 8), x = f[i].value();
+            const Vec8 w = weights(i, c), x = f[i].value();
             Vec8 t = g[i].value();
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
@@ -420,7 +433,7 @@ norm_backward_kernel(const T* dy, const T* h, const float* weight, const T* dh, 
         for (int i = 0; i < VPT; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             if (c >= nv) continue;
-            const Vec8 w = load8(weight + c * 8), y = g[i].value();
+            const Vec8 w = weights(i, c), y = g[i].value();
             Vec8 x = f[i].value(), out = y;
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
@@ -523,11 +536,11 @@ static int ring_bytes(int N, int elem) {
     const int bytes = kNormStages * 3 * N * elem;
     return bytes <= 100 * 1024 ? bytes : 0;
 }
-// Blocks of the backward pass: what an SM holds (about 1024 threads, and the rings),
+// Blocks of the backward pass: what an SM holds (about 640 threads, and the rings),
 // so that enough rows are in flight, and no more, so that few partial sums leave.
 static int backward_blocks(long long rows, int N, int elem) {
     const int threads = row_threads(N, vectors_per_thread(N)), ring = ring_bytes(N, elem);
-    int each = threads >= 1024 ? 1 : 1024 / threads;
+    int each = threads >= 640 ? 1 : 640 / threads;
     if (ring && each > 216 * 1024 / (ring + 2048)) each = 216 * 1024 / (ring + 2048);
     const long long most = (long long)kDefaultSmCount * each;
     return (int)(rows < most ? rows : most);
