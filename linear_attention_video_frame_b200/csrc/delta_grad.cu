@@ -241,8 +241,10 @@ delta_reverse_kernel(la_delta in, DeltaGrad grad, DeltaWs ws) {
 // The gradients of all chunks
 // ---------------------------------------------------------------------------
 // A block takes one chunk of one key head and adds up the value heads that
-// share it, in their order.  Warp w: 16 tokens (w % 4) and half of the columns.
-constexpr int kGradThreads = 256;
+// share it, in their order.  Warp w: 16 tokens (w % 4) and a quarter of the columns.
+// Shared memory holds one block an SM, whose warps wait for tiles and products in turn:
+// 232 us for 640 chunks of 128 (8 warps of half the columns: 265).
+constexpr int kGradThreads = 512;
 
 template <int DP>
 struct GradSmem {
@@ -310,10 +312,10 @@ delta_grad_kernel(la_delta in, DeltaGrad grad, DeltaWs ws, int chunks) {
     using Sm = GradSmem<DP>;
     using T = float;
     constexpr int CH = DP / 8, NP = Sm::NP, NI = Sm::NI, kTile = Sm::kTile, kTri = Sm::kTri;
-    constexpr int NT = DP / 16;                 // tiles of a warp's columns
+    constexpr int NT = DP / 32;                 // tiles of a warp's columns
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float gates[kGateRows][kChunk];
-    __shared__ float s_qdq[2][kChunk], s_vdv[kChunk], s_cross[kGradThreads / 32];
+    __shared__ float s_qdq[4][kChunk], s_vdv[kChunk], s_cross[kGradThreads / 32];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rb = warp & 3, ch = warp >> 2, g = lane >> 2, tq = lane & 3;
@@ -325,8 +327,8 @@ delta_grad_kernel(la_delta in, DeltaGrad grad, DeltaWs ws, int chunks) {
     const uint32_t base = smem_u32(smem);
     const uint32_t r0 = base + Sm::o0, r1 = base + Sm::o1, r2 = base + Sm::o2, r3 = base + Sm::o3;
     const int row[2] = {rb * 16 + g, rb * 16 + g + 8};
-    const int col = ch * (DP / 2) + 2 * tq;     // of tile 0
-    const int piece0 = ch * (DP / 16);
+    const int col = ch * (DP / 4) + 2 * tq;     // of tile 0
+    const int piece0 = ch * (DP / 32);
 
     float dq[NT][4], dk[NT][4];
 #pragma unroll
@@ -447,14 +449,14 @@ delta_grad_kernel(la_delta in, DeltaGrad grad, DeltaWs ws, int chunks) {
             if (image == 0) dot_q(qdq, x);
         }
 
-        // dO Z^T and dX Z^T up to the diagonal: this warp's 16 rows, 32 columns
-        Acc dp[4], dn[4];
+        // dO Z^T and dX Z^T up to the diagonal: this warp's 16 rows, 16 columns
+        Acc dp[2], dn[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             dp[i].zero();
             dn[i].zero();
         }
-        if (2 * ch <= rb) {
+        if (ch <= rb) {
 #pragma unroll 1
             for (int ks = 0; ks < D / 16; ++ks) {
                 uint32_t d[NI][4], x[NP][4];
@@ -464,25 +466,19 @@ delta_grad_kernel(la_delta in, DeltaGrad grad, DeltaWs ws, int chunks) {
 #pragma unroll
                 for (int i = 0; i < NP; ++i)
                     ldsm4(x[i], at_rows<CH>(r3 + i * kTile, rb * 16, 2 * ks, lane));
-#pragma unroll
-                for (int np = 0; np < 2; ++np) {
-                    if (2 * ch + np > rb) break;
-                    product_cols<NP, NI, NP, CH>(dp + 2 * np, d, r2, kTile, (2 * ch + np) * 16,
-                                                 2 * ks, lane);
-                    product_cols<NP, NP, NP, CH>(dn + 2 * np, x, r2, kTile, (2 * ch + np) * 16,
-                                                 2 * ks, lane);
-                }
+                product_cols<NP, NI, NP, CH>(dp, d, r2, kTile, ch * 16, 2 * ks, lane);
+                product_cols<NP, NP, NP, CH>(dn, x, r2, kTile, ch * 16, 2 * ks, lane);
             }
         }
-        // dV, dbeta and v . dV: four threads a row
+        // dV, dbeta and v . dV: eight threads a row
         {
-            const int r = tid >> 2;
+            const int r = tid >> 3;
             const T* v = static_cast<const T*>(in.v) + row3(in.v_stride).at(b, h, t0) +
                          r * in.v_stride[2];
             T* dv = static_cast<T*>(grad.dv) + (gate_at + r) * D;
             const float beta = gates[2][r];
             float xz = 0.f, vdv = 0.f;
-            for (int c = tid & 3; c * 8 < D; c += 4) {
+            for (int c = tid & 7; c * 8 < D; c += 8) {
                 float x[8], z[8], f[8];
                 fetch_planes<NP>(x, reinterpret_cast<const __nv_bfloat16*>(
                                         smem + Sm::o3 + tile_at<CH>(r, c)),
@@ -500,11 +496,11 @@ delta_grad_kernel(la_delta in, DeltaGrad grad, DeltaWs ws, int chunks) {
                 if (r < rows) put8(dv + c * 8, x);
             }
 #pragma unroll
-            for (int d = 1; d < 4; d <<= 1) {
+            for (int d = 1; d < 8; d <<= 1) {
                 xz += __shfl_xor_sync(~0u, xz, d);
                 vdv += __shfl_xor_sync(~0u, vdv, d);
             }
-            if ((tid & 3) == 0) {
+            if ((tid & 7) == 0) {
                 s_vdv[r] = vdv;
                 if (r < rows) grad.dbeta[gate_at + r] = r < on ? xz : 0.f;
             }
@@ -512,13 +508,12 @@ delta_grad_kernel(la_delta in, DeltaGrad grad, DeltaWs ws, int chunks) {
         __syncthreads();                        // dO, Z and dX have been read
 
         // dP o E and N' + N'^T as split tiles
-        if (2 * ch <= rb) {
+        if (ch <= rb) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (2 * ch + i / 2 > rb) break;
+            for (int i = 0; i < 2; ++i) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int ti = row[e >> 1], tj = ch * 32 + i * 8 + 2 * tq + (e & 1);
+                    const int ti = row[e >> 1], tj = ch * 16 + i * 8 + 2 * tq + (e & 1);
                     // above the diagonal E may overflow: it is selected away
                     const float E = exp2_sum(gates[3][ti], gates[4][ti], gates[3][tj],
                                              gates[4][tj]) * gates[2][tj];
@@ -627,7 +622,8 @@ delta_grad_kernel(la_delta in, DeltaGrad grad, DeltaWs ws, int chunks) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
-                s[i] = (double)s_qdq[0][t] + (double)s_qdq[1][t] - (double)s_vdv[t];
+                s[i] = ((double)s_qdq[0][t] + (double)s_qdq[1][t]) +
+                       ((double)s_qdq[2][t] + (double)s_qdq[3][t]) - (double)s_vdv[t];
             }
             if (lane == 31)
                 for (int i = 0; i < kGradThreads / 32; ++i) s[1] += (double)s_cross[i];

@@ -12,10 +12,9 @@
 // threads holds 16 KB of a 128-row state: 8 threads side by side take one 128-byte
 // row piece, so every access is a full line, each thread has its eight 16-byte loads
 // in flight at once, and few warps wait for one another at a block's two barriers.
-// 192 x 32 heads of 128: 125 to 130 us, 6.2 TB/s and more (256 threads of four
-// loads: 157).  Eight
-// blocks an SM, which leaves a thread 64 registers; with six of 80 heads of 112 and 256
-// take a tenth longer.
+// 192 x 32 heads of 128: 125 to 130 us, 6.2 TB/s and more (256 threads of four loads:
+// 157).  Eight blocks an SM leave a thread 64 registers; with six of 80, heads of 112
+// and 256 take a tenth longer.
 #include <cuda_bf16.h>
 
 #include "token.cuh"
