@@ -232,7 +232,8 @@ def la_gated_delta_step(q, k, v, log_alpha, beta, state_in, k_scale: float = 1.0
     if o is None:
         o = _new_rows(v, lengths)
     os = _rows(o, "o", shape, q.dtype, device)
-    end = _full(state_out, "state_out", (B, Hv, D, D), torch.float32, device)
+    end = state_in.data_ptr() if state_out is state_in else \
+        _full(state_out, "state_out", (B, Hv, D, D), torch.float32, device)
     st = lib.la_gated_delta_step(a, o.data_ptr(), _pack_strides(*os), end,
                                  _raw_stream(stream, device))
     if st != LA_OK:
@@ -255,11 +256,18 @@ def la_gated_delta_rule_backward(q, k, v, log_alpha, beta, do, k_scale: float = 
     kshape, dtype, f32 = q.shape, q.dtype, torch.float32
     dos = _rows(do, "do", vshape, dtype, device)
 
-    def out(t, shape, dt):
-        return q.new_empty(shape, dtype=dt) if t is None else t
+    def out(t, name, like):
+        """The gradient of `like` and its address."""
+        if t is None:
+            t = torch.empty_like(like, memory_format=torch.contiguous_format)
+            return t, t.data_ptr()
+        return t, _full(t, name, like.shape, like.dtype, device)
 
-    dq, dk, dv = out(dq, kshape, dtype), out(dk, kshape, dtype), out(dv, vshape, dtype)
-    dlog_alpha, dbeta = out(dlog_alpha, vshape[:3], f32), out(dbeta, vshape[:3], f32)
+    dq, pdq = out(dq, "dq", q)
+    dk, pdk = out(dk, "dk", k)
+    dv, pdv = out(dv, "dv", v)
+    dlog_alpha, pdlog = out(dlog_alpha, "dlog_alpha", log_alpha)
+    dbeta, pdbeta = out(dbeta, "dbeta", beta)
     need = _delta_need(1, code, B, kshape[1], Hv, T, D)
     if need == 0:
         raise LaScanError(LA_ERR_UNSUPPORTED, "la_gated_delta_rule_backward")
@@ -267,11 +275,7 @@ def la_gated_delta_rule_backward(q, k, v, log_alpha, beta, do, k_scale: float = 
     st = lib.la_gated_delta_rule_backward(
         a, do.data_ptr(), _pack_strides(*dos),
         _full(dstate_out, "dstate_out", (B, Hv, D, D), f32, device),
-        _full(dq, "dq", kshape, dtype, device), _full(dk, "dk", kshape, dtype, device),
-        _full(dv, "dv", vshape, dtype, device),
-        _full(dlog_alpha, "dlog_alpha", vshape[:3], f32, device),
-        _full(dbeta, "dbeta", vshape[:3], f32, device),
-        _full(dstate_in, "dstate_in", (B, Hv, D, D), f32, device),
+        pdq, pdk, pdv, pdlog, pdbeta, _full(dstate_in, "dstate_in", (B, Hv, D, D), f32, device),
         workspace.data_ptr(), workspace.numel(), _raw_stream(stream, device))
     if st != LA_OK:
         _raise(st, "la_gated_delta_rule_backward")
