@@ -11,8 +11,9 @@
 // (16) and of the key rows.  Three load warps keep the next chunk in flight.
 //
 // The chain of products and register work bounds it, not its bytes: 2300 cycles of
-// products and as many of register work depend on one another, 3.3 to 3.8 us a chunk
-// in all (80 heads of 128, 32 chunks: 118 us, DRAM at 24 % of its peak).
+// products and as many of register work depend on one another, 4800 cycles a chunk in
+// all, with outputs 5300 to 6000 (80 heads of 128, 32 chunks: 118 us, DRAM at 24 % of
+// its peak).
 #include "delta_tc.cuh"
 
 namespace la {
