@@ -90,7 +90,9 @@ LA_API la_status la_gated_delta_rule(const la_delta* in, void* o, const long lon
  * dq, dk     out: [B, Hk, T, D] of dtype dt, contiguous: summed over the value
  *                 heads that share the key head, in their order.
  * dv         out: [B, Hv, T, D] of dtype dt, contiguous.
- * dlog_alpha, dbeta out: [B, Hv, T] f32.
+ * dlog_alpha, dbeta out: [B, Hv, T] f32.  dlog_alpha is exactly 0 where there is no
+ *                 state to scale: at a token that forgets it, and at the first one
+ *                 without in->state_in.
  * dstate_in  out: [B, Hv, D, D] f32 or NULL; may be dstate_out.
  * Gradients of rows behind a sequence's length are 0.
  * D <= 128, else LA_ERR_UNSUPPORTED.

@@ -363,3 +363,15 @@ def test_status_of_a_call(T, D, dtype):
         ws = la.delta_workspace_for(backward, code, 1, 2, 2, T, D).fill_(255)
         (_backward if backward else _forward)(x, workspace=ws)
         assert la.la_query_device_status(ws) == la.LA_OK
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,D", [(1, 64), (1, 128), (70, 48)])
+def test_first_token_has_no_state_to_forget(T, D, dtype):
+    """log_alpha of a first token scales a state of zeros: its gradient is 0, not the rounding
+    of terms that cancel."""
+    x = delta_inputs(2, 2, 4, T, D, dtype, seed=70 + T, state=False)
+    assert x["state"] is None
+    g = _backward(x)["log_alpha"]
+    assert (g[:, :, 0] == 0).all()
+    assert T == 1 or (g[:, :, 1:] != 0).any()
