@@ -8,6 +8,10 @@ and v, o ``[B, Hv, T, D]`` (bfloat16 or float32) may be strided views as long
 as the D values of a row are contiguous, for example ``[B, T, H, D]``
 transposed; log_alpha, beta ``[B, Hv, T]`` and states ``[B, Hv, D, D]`` are
 contiguous float32; lengths ``[B]`` is int32 or None.
+
+``stream`` is a torch stream or the address of a CUDA stream (default: the current
+one).  Inputs, and outputs that are given, have to be ready on it; a call's new
+outputs are made on it and may be used on the current stream once that waits for it.
 """
 from __future__ import annotations
 
@@ -17,7 +21,7 @@ import struct
 
 import torch
 
-from . import (LA_ERR_UNSUPPORTED, LA_OK, LaScanError, _check, _dtype_code, _raise, _stream, lib)
+from . import LA_ERR_UNSUPPORTED, LA_OK, LaScanError, _check, _dtype_code, _raise, lib
 
 __all__ = [
     "LaDelta", "la_gated_delta_rule", "la_gated_delta_rule_backward", "la_gated_delta_step",
@@ -111,10 +115,27 @@ def _here(t: torch.Tensor, name: str) -> int:
     return device
 
 
-def _raw_stream(stream, device: int):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
-    return _stream(stream)
+def _raw_stream(device: int):
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _elsewhere(stream, call, *args, **kw):
+    """`call` with `stream` as the current stream, or NotImplemented where it is that already.
+    A call's new tensors so come from the stream's own memory, are filled on it, and go back
+    to it when they are let go, in the order of its kernels; the stream that is current now
+    is where the caller uses them, so their memory waits for it as well."""
+    here = torch.cuda.current_stream()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), here.device)
+    if stream.cuda_stream == here.cuda_stream:
+        return NotImplemented
+    with torch.cuda.stream(stream):
+        result = call(*args, **kw)
+    given = {id(t) for t in (*args, *kw.values())}
+    for t in result if isinstance(result, tuple) else (result,):
+        if t is not None and id(t) not in given:
+            t.record_stream(here)
+    return result
 
 
 def _full(t, name: str, shape, dtype, device):
@@ -128,14 +149,10 @@ def _full(t, name: str, shape, dtype, device):
     return t.data_ptr()
 
 
-def _space(workspace, need: int, like: torch.Tensor, stream):
-    """The workspace of a call: the given one, or a new one.  A new one is let go when the call
-    returns, so the allocator has to know of another stream that its kernels run on."""
+def _space(workspace, need: int, like: torch.Tensor):
+    """The workspace of a call: the given one, or a new one."""
     if workspace is None:
         workspace = like.new_empty((need,), dtype=torch.uint8)
-        if stream is not None:
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                    else torch.cuda.ExternalStream(int(stream), like.device))
     elif workspace.device != like.device:
         raise ValueError(f"workspace is on {workspace.device}, expected {like.device}")
     return workspace
@@ -195,6 +212,11 @@ def la_gated_delta_rule(q, k, v, log_alpha, beta, k_scale: float = 1.0, q_scale:
     """Gated delta rule over T tokens: ``S_t = alpha_t (I - beta_t k k^T) S_{t-1} + beta_t k v^T``,
     ``o_t = q S_t`` with ``alpha = exp(log_alpha)`` (see include/la_token.h).  Returns o; rows
     behind a sequence's length are left as they were in a given o, 0 in a new one."""
+    if stream is not None:
+        done = _elsewhere(stream, la_gated_delta_rule, q, k, v, log_alpha, beta, k_scale, q_scale,
+                          o, state_in, state_out, lengths, workspace)
+        if done is not NotImplemented:
+            return done
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k and v are [B, H, T, D]")
     device = _here(q, "q")
@@ -207,9 +229,9 @@ def la_gated_delta_rule(q, k, v, log_alpha, beta, k_scale: float = 1.0, q_scale:
     need = _delta_need(0, code, B, q.shape[1], Hv, T, D)
     if need == 0:
         raise LaScanError(LA_ERR_UNSUPPORTED, "la_gated_delta_rule")
-    workspace = _space(workspace, need, q, stream)
+    workspace = _space(workspace, need, q)
     st = lib.la_gated_delta_rule(a, o.data_ptr(), _pack_strides(*os), end, workspace.data_ptr(),
-                                 workspace.numel(), _raw_stream(stream, device))
+                                 workspace.numel(), _raw_stream(device))
     if st != LA_OK:
         _raise(st, "la_gated_delta_rule")
     return o
@@ -220,6 +242,11 @@ def la_gated_delta_step(q, k, v, log_alpha, beta, state_in, k_scale: float = 1.0
     """One token of the gated delta rule for every sequence: q, k ``[B, Hk, D]``, v, o
     ``[B, Hv, D]``, log_alpha, beta ``[B, Hv]``.  state_out (default: state_in, in place) gets
     the new state.  A sequence of length 0 keeps its state and its row of o."""
+    if stream is not None:
+        done = _elsewhere(stream, la_gated_delta_step, q, k, v, log_alpha, beta, state_in, k_scale,
+                          q_scale, o, state_out, lengths)
+        if done is not NotImplemented:
+            return done
     if q.dim() != 3 or v.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v of a step are [B, H, D]")
     if state_out is None:
@@ -235,7 +262,7 @@ def la_gated_delta_step(q, k, v, log_alpha, beta, state_in, k_scale: float = 1.0
     end = state_in.data_ptr() if state_out is state_in else \
         _full(state_out, "state_out", (B, Hv, D, D), torch.float32, device)
     st = lib.la_gated_delta_step(a, o.data_ptr(), _pack_strides(*os), end,
-                                 _raw_stream(stream, device))
+                                 _raw_stream(device))
     if st != LA_OK:
         _raise(st, "la_gated_delta_step")
     return o
@@ -248,6 +275,12 @@ def la_gated_delta_rule_backward(q, k, v, log_alpha, beta, do, k_scale: float = 
     """Gradients (dq, dk, dv, dlog_alpha, dbeta) of la_gated_delta_rule for the gradient `do` of
     its output and `dstate_out` of its final state; dstate_in (if given) gets the initial
     state's.  Gradients of rows behind a sequence's length are 0."""
+    if stream is not None:
+        done = _elsewhere(stream, la_gated_delta_rule_backward, q, k, v, log_alpha, beta, do,
+                          k_scale, q_scale, state_in, dstate_out, dq, dk, dv, dlog_alpha, dbeta,
+                          dstate_in, lengths, workspace)
+        if done is not NotImplemented:
+            return done
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k and v are [B, H, T, D]")
     device = _here(q, "q")
@@ -271,12 +304,12 @@ def la_gated_delta_rule_backward(q, k, v, log_alpha, beta, do, k_scale: float = 
     need = _delta_need(1, code, B, kshape[1], Hv, T, D)
     if need == 0:
         raise LaScanError(LA_ERR_UNSUPPORTED, "la_gated_delta_rule_backward")
-    workspace = _space(workspace, need, q, stream)
+    workspace = _space(workspace, need, q)
     st = lib.la_gated_delta_rule_backward(
         a, do.data_ptr(), _pack_strides(*dos),
         _full(dstate_out, "dstate_out", (B, Hv, D, D), f32, device),
         pdq, pdk, pdv, pdlog, pdbeta, _full(dstate_in, "dstate_in", (B, Hv, D, D), f32, device),
-        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, device))
+        workspace.data_ptr(), workspace.numel(), _raw_stream(device))
     if st != LA_OK:
         _raise(st, "la_gated_delta_rule_backward")
     return dq, dk, dv, dlog_alpha, dbeta
@@ -288,6 +321,10 @@ def la_add_rms_norm_fp8(x, residual, weight, eps: float = 1e-6, group: int = 128
     None), weight ``[N]`` float32.  Returns (y float8_e4m3fn ``[..., N]``, scale float32
     ``[..., ceil(N / group)]`` (group = 0: ``[..., 1]``), h = x + residual as stored, which is x
     itself without a residual).  ``y.float() * scale`` (each scale over its group) is the norm."""
+    if stream is not None:
+        done = _elsewhere(stream, la_add_rms_norm_fp8, x, residual, weight, eps, group, h, y, scale)
+        if done is not NotImplemented:
+            return done
     shape, dtype = x.shape, x.dtype
     N = shape[-1]
     dt = _dtype_code(x)
@@ -315,7 +352,7 @@ def la_add_rms_norm_fp8(x, residual, weight, eps: float = 1e-6, group: int = 128
     else:
         ps = _full(scale, "scale", groups, torch.float32, device)
     st = lib.la_add_rms_norm_fp8(px, pr, pw, ph, py, ps, dt, x.numel() // N if N else 0, N, group,
-                                 eps, _raw_stream(stream, device))
+                                 eps, _raw_stream(device))
     if st != LA_OK:
         _raise(st, "la_add_rms_norm_fp8")
     return y, scale, x if h is None else h
@@ -327,6 +364,11 @@ def la_add_rms_norm_backward(dy, h, weight, dh=None, eps: float = 1e-6, dx=None,
     rounding passed straight through), h as the forward pass returned it and `dh`, the gradient
     that h gets from elsewhere.  dx is the gradient of x and of residual alike; dweight is None
     when need_dweight is False."""
+    if stream is not None:
+        done = _elsewhere(stream, la_add_rms_norm_backward, dy, h, weight, dh, eps, dx, dweight,
+                          need_dweight, workspace)
+        if done is not NotImplemented:
+            return done
     shape, dtype = h.shape, h.dtype
     N = shape[-1]
     dt = _dtype_code(h)
@@ -345,12 +387,12 @@ def la_add_rms_norm_backward(dy, h, weight, dh=None, eps: float = 1e-6, dx=None,
         if dweight is None:
             dweight = torch.empty_like(weight)
         pdw = _full(dweight, "dweight", (N,), torch.float32, device)
-        workspace = _space(workspace, _norm_need(rows, N), h, stream)
+        workspace = _space(workspace, _norm_need(rows, N), h)
         space, size = workspace.data_ptr(), workspace.numel()
     else:
         dweight = None
     st = lib.la_add_rms_norm_backward(pdy, ph, pw, pdh, pdx, pdw, dt, rows, N, eps, space, size,
-                                      _raw_stream(stream, device))
+                                      _raw_stream(device))
     if st != LA_OK:
         _raise(st, "la_add_rms_norm_backward")
     return dx, dweight

@@ -375,3 +375,95 @@ def test_first_token_has_no_state_to_forget(T, D, dtype):
     g = _backward(x)["log_alpha"]
     assert (g[:, :, 0] == 0).all()
     assert T == 1 or (g[:, :, 1:] != 0).any()
+
+
+def _hold(stream=None):
+    """Keeps a stream busy for some milliseconds."""
+    with torch.cuda.stream(stream or torch.cuda.current_stream()):
+        torch.cuda._sleep(30_000_000)
+
+
+# one token, token by token, by chunks
+@pytest.mark.parametrize("T", [1, 10, 200])
+def test_new_output_is_filled_on_the_stream_of_the_call(T):
+    """Rows behind a sequence are 0 in a new output: its fill must not come after the kernels,
+    whatever the current stream is busy with."""
+    x = delta_inputs(2, 2, 4, T, 64, seed=80 + T, lengths=[T, T // 2])
+    want = torch.zeros_like(x["v"])
+    _forward(x, o=want)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _hold()
+    o, end = _forward(x, stream=side)
+    one = None
+    if T == 1:
+        a = [t[:, :, 0] for t in _args(x)]
+        a[3], a[4] = a[3].contiguous(), a[4].contiguous()
+        torch.cuda.synchronize()
+        _hold()
+        one = la.la_gated_delta_step(*a, x["state"], state_out=torch.empty_like(end), **_kw(x),
+                                     stream=side)
+    torch.cuda.synchronize()
+    assert _same(o, want)
+    assert one is None or _same(one, want[:, :, 0])
+
+
+def test_new_tensors_of_a_call_on_another_stream():
+    """What the current stream has let go but still works on is not given to the call; what the
+    call's caller lets go is not given to the current stream; and what the current stream still
+    reads is not given to the next call."""
+    x, z = delta_inputs(1, 2, 2, 700, 128, seed=91), delta_inputs(1, 2, 2, 700, 128, seed=92)
+    want, want_z = _forward(x)[0], _forward(z)[0]
+    grads = _backward(x)
+    side = torch.cuda.Stream()
+
+    def call(x, **kw):
+        return la.la_gated_delta_rule(*_args(x), state_in=x["state"], **_kw(x), **kw)
+
+    def back(x, **kw):
+        return la.la_gated_delta_rule_backward(*_args(x), x["do"], state_in=x["state"],
+                                               dstate_out=x["dstate"], **_kw(x), **kw)
+
+    for f, r in ((call, (want,)), (back, [grads[n] for n in NAMES[:5]])):
+        junk = [torch.empty_like(t, memory_format=torch.contiguous_format) for t in r]
+        torch.cuda.synchronize()
+        _hold()
+        for t in junk:
+            t.fill_(7.0)
+        del junk, t
+        got = f(x, stream=side)
+        torch.cuda.synchronize()
+        got = got if isinstance(got, tuple) else (got,)
+        assert all(_same(a, b) for a, b in zip(got, r))
+        del got
+
+    _hold(side)
+    call(x, stream=side)                        # let go at once
+    after = [torch.full_like(want, 3.0) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all((t == 3.0).all() for t in after)
+    del after
+
+    o = call(x, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    _hold()
+    copy = o.clone()
+    del o
+    others = [call(z, stream=side) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert _same(copy, want) and all(_same(t, want_z) for t in others)
+
+
+def test_streams_by_their_addresses():
+    """A stream may be given as the address of its CUDA stream."""
+    x = delta_inputs(1, 2, 2, 200, 64, seed=93, lengths=[150])
+    want = torch.zeros_like(x["v"])
+    _forward(x, o=want)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _hold()
+    o, _ = _forward(x, stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    assert _same(o, want)
+    o, _ = _forward(x, stream=torch.cuda.current_stream().cuda_stream)
+    assert _same(o, want)

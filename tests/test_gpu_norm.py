@@ -210,3 +210,31 @@ def test_half_block_of_a_decoder():
     # (delta_bound(100) = 3e-5) of its largest value
     for got, r in zip((dx, dw1, dw2, grads[3], grads[4]), ref):
         assert (got.double().cpu() - r).abs().max() <= 4e-4 * r.abs().max()
+
+
+def test_new_outputs_on_another_stream():
+    """New outputs of a call on a stream that is not the current one: not what the current
+    stream still writes to, and not given to it before the call has run."""
+    x, r, w = _inputs(300, 640, BF16, seed=17)
+    want = la.la_add_rms_norm_fp8(x, r, w)
+    dx, dw = la.la_add_rms_norm_backward(x, r, w)
+    side = torch.cuda.Stream()
+    junk = [torch.empty_like(t) for t in (*want, dx, dw)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(30_000_000)
+    for t in junk:
+        t.view(torch.uint8).fill_(7)
+    del junk, t
+    got = (*la.la_add_rms_norm_fp8(x, r, w, stream=side),
+           *la.la_add_rms_norm_backward(x, r, w, stream=side))
+    torch.cuda.synchronize()
+    for a, b in zip(got, (*want, dx, dw)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(30_000_000)
+    y, scale, _ = la.la_add_rms_norm_fp8(x, r, w, stream=side)
+    del _
+    after = [torch.full_like(x, 3.0) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all((t == 3.0).all() for t in after)
+    assert torch.equal(y.view(torch.uint8), want[0].view(torch.uint8))
