@@ -127,7 +127,7 @@ LA_API const char* la_delta_plan(int backward, la_dtype dt, int B, int Hk, int H
  * Residual addition, RMSNorm and an output in e4m3 with scales, per row of N:
  *     h = round_dt(x + residual)                   (h = x without a residual)
  *     y = h / sqrt(mean(h^2) + eps) * weight
- *     scale = max |y| / 448 over each group of columns (1 where that is 0)
+ *     scale = max |y| / 448 over each group of columns (1 where that is 0 in float32)
  *     y8 = e4m3(y / scale), rounded to nearest even
  * h is normalised as it is stored, so that the backward pass sees the same h.
  * group = 128: a scale for each 128 columns (the last group may be shorter);

@@ -153,9 +153,10 @@ __device__ __forceinline__ float norm8(Vec8& y, float r, const float* weight) {
     return top;
 }
 // The scale of a largest magnitude, and its reciprocal or 0 where that is to be
-// divided by.  (NaN and infinity divide as well.)
+// divided by.  (NaN and infinity divide as well.)  A quotient that underflows to 0 is
+// as good as 0: dividing by it would make NaN of the group's zeros.
 __device__ __forceinline__ float scale_of(float top, float& inv) {
-    const float s = top == 0.f ? 1.f : top / kE4m3Max;
+    const float q = top / kE4m3Max, s = q == 0.f ? 1.f : q;
     inv = s > 1e-36f && s < 1e36f ? 1.f / s : 0.f;
     return s;
 }

@@ -238,3 +238,16 @@ def test_new_outputs_on_another_stream():
     torch.cuda.synchronize()
     assert all((t == 3.0).all() for t in after)
     assert torch.equal(y.view(torch.uint8), want[0].view(torch.uint8))
+
+
+@pytest.mark.parametrize("N", [256, 1040])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("group", [0, 128])
+def test_scale_that_underflows(N, dtype, group):
+    """max |y| / 448 may be 0 in float32 though y is not: the scale is 1 there as well, and
+    the values, far below e4m3's smallest, are 0."""
+    x, r, w = _inputs(3, N, dtype, seed=N)
+    x[:, ::3], r[:, ::3] = 0.0, 0.0
+    y, scale, h = la.la_add_rms_norm_fp8(x, r, w * 1e-44, eps=EPS, group=group)
+    assert (scale == 1).all()
+    assert (y.float() == 0).all()
