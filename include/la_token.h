@@ -132,7 +132,8 @@ LA_API const char* la_delta_plan(int backward, la_dtype dt, int B, int Hk, int H
  * h is normalised as it is stored, so that the backward pass sees the same h.
  * group = 128: a scale for each 128 columns (the last group may be shorter);
  * group = 0: one scale for the row.  A row that holds NaN or infinity gives
- * NaN in what it reaches.
+ * NaN in what it reaches.  The squares are summed in float32: a row whose sum of
+ * squares is above 3.4e38 gives zeros, and eps = 0 needs one of at least 1e-37.
  * x, residual in : [rows, N] of dtype dt; residual may be NULL.
  * weight      in : [N] f32.
  * h           out: [rows, N] of dtype dt or NULL; may be x or residual.

@@ -428,7 +428,9 @@ norm_backward_kernel(const T* dy, const T* h, const float* weight, const T* dh, 
             buf ^= 1;
         }
         const float r = 1.f / sqrtf(ss / (float)N + eps);
-        const float s = -(r * r * r * (tf / (float)N));
+        // dx = r t - (h r) (r (r mean(t h))): of factors that are as large as their product
+        // (r^3 would leave float32's range at a root mean square of 1e13, or of 1e-13)
+        const float s = -(r * (r * (tf / (float)N)));
         if (STAGES) fetch();               // again, so that registers are free meanwhile
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -440,8 +442,8 @@ norm_backward_kernel(const T* dy, const T* h, const float* weight, const T* dh, 
             for (int j = 0; j < 8; j += 2) {
                 mul2(out.x[j], out.x[j + 1], w.x[j], w.x[j + 1]);
                 mul2(out.x[j], out.x[j + 1], r, r);
-                fma2(out.x[j], out.x[j + 1], x.x[j], x.x[j + 1], s, s);
                 mul2(x.x[j], x.x[j + 1], r, r);
+                fma2(out.x[j], out.x[j + 1], x.x[j], x.x[j + 1], s, s);
                 fma2(dw[i].x[j], dw[i].x[j + 1], y.x[j], y.x[j + 1], x.x[j], x.x[j + 1]);
             }
             if (dh) {

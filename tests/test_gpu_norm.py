@@ -251,3 +251,35 @@ def test_scale_that_underflows(N, dtype, group):
     y, scale, h = la.la_add_rms_norm_fp8(x, r, w * 1e-44, eps=EPS, group=group)
     assert (scale == 1).all()
     assert (y.float() == 0).all()
+
+
+def _check_backward(dy, h, w, dh, eps, dx, dw=None, steps=0):
+    """dx, and dw as a sum of `steps` roundings, against float64."""
+    h64, w64 = h.double().requires_grad_(), w.double().requires_grad_()
+    y = h64 / (h64.square().mean(-1, keepdim=True) + eps).sqrt() * w64
+    rx, rw = torch.autograd.grad((y * dy.double()).sum(), (h64, w64))
+    h64 = h64.detach()
+    r = 1 / (h64.square().mean(-1, keepdim=True) + eps).sqrt()
+    t = (dy.double() * w.double()).abs()
+    # dx is three terms, each known to the bounds of its sums and roundings
+    terms = r * t + h64.abs() * r ** 3 * (t * h64.abs()).mean(-1, keepdim=True)
+    if dh is not None:
+        rx, terms = rx + dh.double(), terms + dh.double().abs()
+    b = 4 * _sum_bound(h.shape[-1])
+    half = torch.finfo(h.dtype).eps / 2 if h.dtype != F32 else 0.0
+    assert ((dx.double() - rx).abs() <= half * rx.abs() + (1 + half) * b * terms).all()
+    if dw is not None:
+        each = (dy.double() * h64 * r).abs().sum(0)
+        assert ((dw.double() - rw).abs() <= (steps * U + 2 * b) * each).all()
+
+
+@pytest.mark.parametrize("N", [144, 1040, 4800, 8208])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("size,eps", [(1e13, EPS), (1e15, EPS), (1e17, EPS), (1e-15, 0.0),
+                                      (1e-17, 0.0)])
+def test_backward_of_large_and_small_rows(N, dtype, size, eps):
+    """The cube of 1 / rms leaves float32's range long before the gradient does."""
+    h, dy, w = _inputs(3, N, dtype, seed=N)
+    h = (h.float() * size).to(dtype)
+    dx, dw = la.la_add_rms_norm_backward(dy, h, w, eps=eps)
+    _check_backward(dy, h, w, None, eps, dx, dw, steps=3 + 40)
