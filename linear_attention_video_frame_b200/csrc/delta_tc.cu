@@ -43,6 +43,7 @@ struct ChainArgs {
     Row3 os;
     float* state_out;
     int pass;                       // 0: whole chains; 1, 2: the passes over segments
+    int skip_rows;                  // tests: chunk of head 0 whose rows are not announced, or -1
 };
 
 // The part of a head's chain that a block runs.
@@ -305,7 +306,7 @@ delta_tc_chain_kernel(ChainArgs args) {
             const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(in.q) + q3.at(b, hk, 32 * role);
             for (int i = 0; i < n; ++i) {
                 const int c = c0 + i, st = i & 1, t0 = c * kChunk, rows = len - t0;
-                if (i >= 2) tc::mbar_wait(&empty[st], ((i >> 1) - 1) & 1, ab, 7);
+                if (i >= 2 && !tc::mbar_wait(&empty[st], ((i >> 1) - 1) & 1, ab, 7)) break;
                 const uint32_t sa = smem_u32(smem + st * Sm::kStage);
                 if (role == 0) {
                     load_tile(sa + Sm::oKQ, Sm::kHalf, src + t0 * rows3.t, rows3.t, rows, D,
@@ -327,22 +328,27 @@ delta_tc_chain_kernel(ChainArgs args) {
                                    role == 0 ? Sm::kKt : Sm::kPt, lane);
                 cp_wait<0>();
                 tc::fence_proxy_async_smem();
-                tc::mbar_arrive(&full[st]);
+                if (role == 1 || head > 0 || c != args.skip_rows) tc::mbar_arrive(&full[st]);
             }
         } else if (lane == 0) {
+            // A barrier is armed again only once its last copy was read, so that after an
+            // abort at most one copy to each is in flight.
+            int kt = -1, pt = -1;                       // the chunks whose copies went out last
             for (int i = 0; i < n; ++i) {
-                if (i >= 1) tc::mbar_wait(&done_upd[kHalves - 1], (i - 1) & 1, ab, 8);
+                if (i >= 1 && !tc::mbar_wait(&done_upd[kHalves - 1], (i - 1) & 1, ab, 8)) break;
                 tc::mbar_expect_tx(&full_kt, Sm::kKt);
                 tc::bulk_load(smem + Sm::oKt, ws.Kt(head, c0 + i), Sm::kKt, &full_kt);
+                kt = i;
                 if (!emit) continue;
-                if (i >= 1) tc::mbar_wait(&done_px, (i - 1) & 1, ab, 9);
+                if (i >= 1 && !tc::mbar_wait(&done_px, (i - 1) & 1, ab, 9)) break;
                 tc::mbar_expect_tx(&full_pt, Sm::kPt);
                 tc::bulk_load(smem + Sm::oPt, STATES ? ws.L(head, c0 + i) : ws.P(head, c0 + i),
                               Sm::kPt, &full_pt);
+                pt = i;
             }
-            if (n > 0 && tc::aborted(ab)) {
-                tc::mbar_drain(&full_kt, (n - 1) & 1);
-                if (emit) tc::mbar_drain(&full_pt, (n - 1) & 1);
+            if (tc::aborted(ab)) {
+                if (kt >= 0) tc::mbar_drain(&full_kt, kt & 1);
+                if (pt >= 0) tc::mbar_drain(&full_pt, pt & 1);
             }
         }
     } else {
@@ -422,7 +428,7 @@ cudaError_t chain(const ChainArgs& a, cudaStream_t st) {
 
 cudaError_t launch_delta_tc_chain(const la_delta& in, const DeltaWs& ws, void* o, Row3 os,
                                   float* state_out, bool states, cudaStream_t st) {
-    const ChainArgs a{in, ws, o, os, state_out, 0};
+    const ChainArgs a{in, ws, o, os, state_out, 0, test_skip_rows(false)};
     if (states) return in.D <= 64 ? chain<64, true>(a, st) : chain<128, true>(a, st);
     return in.D <= 64 ? chain<64, false>(a, st) : chain<128, false>(a, st);
 }

@@ -1,6 +1,8 @@
 // Shared definitions of the token-wise operators (include/la_token.h).
 #pragma once
 
+#include <cstdlib>
+
 #include "common.cuh"
 #include "la_token.h"
 
@@ -32,6 +34,16 @@ __device__ __forceinline__ int seq_len(const int* lengths, int b, int T) {
     if (!lengths) return T;
     const int n = lengths[b];
     return n < 0 ? 0 : (n > T ? T : n);
+}
+
+// For tests of the bounded waits: LA_DELTA_TEST_SKIP_ROWS = c leaves out the arrival that
+// announces the key rows of head 0's chunk c to a forward chain, -1 - c to a reverse one, so
+// that the waits for it run out.  The chunk, or -1.
+inline int test_skip_rows(bool reverse) {
+    const char* e = std::getenv("LA_DELTA_TEST_SKIP_ROWS");
+    if (!e) return -1;
+    const int c = std::atoi(e);
+    return reverse ? -1 - c : c;
 }
 
 // Launchers; each returns the CUDA error of its launches.

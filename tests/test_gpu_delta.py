@@ -467,3 +467,24 @@ def test_streams_by_their_addresses():
     assert _same(o, want)
     o, _ = _forward(x, stream=torch.cuda.current_stream().cuda_stream)
     assert _same(o, want)
+
+
+# long chains by themselves, and in segments, whose second pass starts with the status set
+@pytest.mark.parametrize("Hv,T,D", [(100, 64 * 40, 64), (100, 64 * 30, 128), (1, 1601, 128)])
+@pytest.mark.parametrize("backward,skip", [(False, 2), (True, 2), (True, -3)])
+def test_waits_that_run_out_are_reported(monkeypatch, Hv, T, D, backward, skip):
+    """An arrival that never comes: the waits for it give up, the block ends with its copies and
+    products done, the call's workspace says so, and the next call works."""
+    plan = la.la_delta_plan(backward, la.LA_BF16, 1, Hv, Hv, T, D)
+    assert plan == ("delta_chunked", (4 if backward else 2)) if Hv > 1 else plan[1] > 3
+    x = delta_inputs(1, Hv, Hv, T, D, seed=130)
+    run = _backward if backward else (lambda x, **kw: dict(zip(("o", "end"), _forward(x, **kw))))
+    want = run(x)
+    ws = la.delta_workspace_for(backward, la.LA_BF16, 1, Hv, Hv, T, D)
+    monkeypatch.setenv("LA_DELTA_TEST_SKIP_ROWS", str(skip))
+    run(x, workspace=ws)
+    assert la.la_query_device_status(ws) == la.LA_ERR_TIMEOUT
+    monkeypatch.delenv("LA_DELTA_TEST_SKIP_ROWS")
+    got = run(x, workspace=ws)
+    assert la.la_query_device_status(ws) == la.LA_OK
+    assert all(_same(got[n], want[n]) for n in want)
