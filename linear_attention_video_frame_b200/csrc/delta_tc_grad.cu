@@ -102,7 +102,7 @@ delta_tc_grad_kernel(GradArgs args) {
     constexpr int NK = DP / 4;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = tc::align1024(smem_raw);
-    __shared__ uint64_t done[2];
+    __shared__ uint64_t done[2], done_all;
     __shared__ uint32_t s_tmem, s_abort;
     __shared__ __align__(16) float gates[kGateRows][kChunk];
     __shared__ float s_dbeta[2][kChunk], s_vdv[2][kChunk], s_qdq[4][kChunk], s_cross[kGradWarps];
@@ -144,7 +144,7 @@ delta_tc_grad_kernel(GradArgs args) {
     const tc::Abort ab{&s_abort, ws.status};
     if (tid == 0) {
         s_abort = 0;
-        for (int i = 0; i < 2; ++i) tc::mbar_init(&done[i], 1);
+        for (uint64_t* bar : {&done[0], &done[1], &done_all}) tc::mbar_init(bar, 1);
         tc::fence_mbar_init();
     }
     if (warp == 0) {
@@ -520,8 +520,10 @@ delta_tc_grad_kernel(GradArgs args) {
             }
         }
     }
-    if (warp == 0 && tc::elect_one() && tc::aborted(ab))
-        for (int i = 0; i < 2; ++i) tc::mbar_drain(&done[i], phase[i] ^ 1);
+    if (warp == 0 && tc::elect_one() && tc::aborted(ab)) {
+        tc::mma_commit(&done_all);              // nothing in flight when the memory is freed
+        tc::mbar_drain(&done_all, 0);
+    }
     tc::tc_fence_before();
     __syncthreads();
     if (warp == 0) {

@@ -67,14 +67,16 @@ struct PrepTc {
 };
 
 // A wait of this kernel, which starts before the status word is known to be reset.
-__device__ __forceinline__ void wait_bounded(uint64_t* bar, uint32_t parity, unsigned int* status) {
-    if (tc::mbar_try_wait(bar, parity)) return;
+// False once it ran out.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, unsigned int* status) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = tc::global_timer_ns();
     while (!tc::mbar_try_wait(bar, parity))
         if (tc::global_timer_ns() - t0 > tc::kWaitLimitNs) {
             atomicExch(status, (unsigned)LA_ERR_TIMEOUT);
-            return;
+            return false;
         }
+    return true;
 }
 
 template <int DP, bool BACKWARD>
@@ -85,7 +87,7 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = tc::align1024(smem_raw);
     __shared__ __align__(16) float g_hi[kChunk], g_lo[kChunk], s_beta[kChunk], s_tail[kChunk];
-    __shared__ uint64_t done;
+    __shared__ uint64_t done, done_all;
     __shared__ uint32_t s_tmem;
 
     const int chunk = blockIdx.x % chunks, head = blockIdx.x / chunks;
@@ -123,6 +125,7 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     if (wid == 0) {
         if (lane == 0) {
             tc::mbar_init(&done, 1);
+            tc::mbar_init(&done_all, 1);
             tc::fence_mbar_init();
         }
         __syncwarp();
@@ -148,7 +151,7 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
         tc::mma_commit(&done);
     }
     __syncwarp();
-    wait_bounded(&done, 0, ws.status);
+    bool ok = wait_bounded(&done, 0, ws.status);
     tc::tc_fence_after();
 
     // N (warps 0 and 1) and P (2 and 3), 32 rows each, up to the diagonal
@@ -465,7 +468,7 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
         tc::mma_commit(&done);
     }
     __syncwarp();
-    wait_bounded(&done, 1, ws.status);
+    ok = wait_bounded(&done, 1, ws.status) && ok;
     tc::tc_fence_after();
     // its planes as rows of tokens, over everything
     if (wid < DP / 32)
@@ -484,6 +487,11 @@ delta_tc_prep_kernel(la_delta in, DeltaWs ws, int chunks) {
     tc::tc_fence_before();
     __syncthreads();
     if (wid == 0) {
+        if (!ok && tc::elect_one()) {           // nothing in flight when the memory is freed
+            tc::mma_commit(&done_all);
+            tc::mbar_drain(&done_all, 0);
+        }
+        __syncwarp();
         tc::tc_fence_after();
         tc::tmem_dealloc(tm, 64);
         if (lane == 0) {
