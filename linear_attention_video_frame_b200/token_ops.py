@@ -155,6 +155,8 @@ def _space(workspace, need: int, like: torch.Tensor):
         workspace = like.new_empty((need,), dtype=torch.uint8)
     elif workspace.device != like.device:
         raise ValueError(f"workspace is on {workspace.device}, expected {like.device}")
+    elif not workspace.is_contiguous():         # its elements are counted as its bytes
+        raise ValueError("workspace must be contiguous")
     return workspace
 
 

@@ -134,3 +134,13 @@ def test_binding_checks_tensors():
         la.la_add_rms_norm_fp8(q.half(), None, g)
     with pytest.raises(ValueError):
         la.la_add_rms_norm_fp8(q, None, torch.zeros(64))
+
+
+def test_workspaces_of_a_call():
+    """A given workspace counts by the bytes that lie behind its address."""
+    like, space = torch.zeros(4), la.token_ops._space
+    whole = torch.zeros(512, dtype=torch.uint8)
+    assert space(whole, 256, like) is whole and space(None, 256, like).numel() == 256
+    for view in (torch.zeros(1, dtype=torch.uint8).expand(512), whole[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            space(view, 256, like)
