@@ -22,9 +22,9 @@
  * value heads share a key head when Hv > Hk: value head h reads q and k of
  * head h / (Hv / Hk).
  *
- * log_alpha = -inf forgets the state (as does any value below -128, whose
- * exponential is 0 in float32).  Positive log_alpha is computed as written and
- * may overflow.  NaN and infinities spread to later tokens as the recurrence
+ * log_alpha = -inf forgets the state (as does any value of -104 or less, whose
+ * exponential is 0 in float32).  Positive log_alpha is computed as written and may
+ * overflow, in the chunked kernels where the sum of neighbouring ones passes 88.  NaN and infinities spread to later tokens as the recurrence
  * carries them, and in the chunked kernels also to the earlier tokens of the
  * same 64; rows behind a sequence's length never matter.
  */

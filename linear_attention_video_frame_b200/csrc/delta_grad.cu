@@ -638,10 +638,10 @@ delta_grad_kernel(la_delta in, DeltaGrad grad, DeltaWs ws, int chunks) {
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
                 if (t >= rows) continue;
-                // below kLogAlphaMin the state before the token is forgotten, and before the
+                // where the decay is 0 the state before the token is forgotten, and before the
                 // first one there may be none: exactly 0, where terms of the sum cancel
                 const bool kept = t < on && (t > 0 || chunk > 0 || in.state_in) &&
-                                  !(in.log_alpha[gate_at + t] < kLogAlphaMin);
+                                  !(in.log_alpha[gate_at + t] <= kForgets);
                 grad.dlog_alpha[gate_at + t] = kept ? (float)sum[i] : 0.f;
             }
         }

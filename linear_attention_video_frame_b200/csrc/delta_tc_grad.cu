@@ -511,10 +511,10 @@ delta_tc_grad_kernel(GradArgs args) {
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
                 if (t >= rows) continue;
-                // below kLogAlphaMin the state before the token is forgotten, and before the
+                // where the decay is 0 the state before the token is forgotten, and before the
                 // first one there may be none: exactly 0, where terms of the sum cancel
                 const bool kept = t < on && (t > 0 || chunk > 0 || in.state_in) &&
-                                  !(in.log_alpha[row + t] < kLogAlphaMin);
+                                  !(in.log_alpha[row + t] <= kForgets);
                 grad.dlog_alpha[row + t] = kept ? (float)sum[i] : 0.f;
                 grad.dbeta[row + t] = t < on ? s_dbeta[0][t] + s_dbeta[1][t] : 0.f;
             }

@@ -292,7 +292,7 @@ __device__ __forceinline__ void chunk_gates(const RawGates& raw, float* gates, f
     const float* bt = raw.beta;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        s[i] = raw.g[i] < kLogAlphaMin ? kLogAlphaMin : raw.g[i];      // keeps NaN
+        s[i] = raw.g[i] <= kForgets ? kForgetSum : raw.g[i];           // keeps NaN
     s[1] += s[0];
     double run = s[1];
 #pragma unroll

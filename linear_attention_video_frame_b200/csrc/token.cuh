@@ -10,9 +10,10 @@ namespace la {
 
 // Tokens of one chunk of the chunked gated delta rule.
 constexpr int kChunk = 64;
-// Below this log decay the decay is 0 in float32; clamping there keeps the
-// running sums of a chunk (at most 64 terms) finite.
-constexpr float kLogAlphaMin = -128.f;
+// At this log decay and below, the decay is 0 in float32 (2^-150 is e^-103.97): the token
+// forgets the state.  In the running sums of a chunk it counts as kForgetSum, so that they
+// stay finite and nothing comes back with the growth of 63 later tokens (e^88.7 each at most).
+constexpr float kForgets = -104.f, kForgetSum = -6000.f;
 
 struct DeltaGrad {           // outputs and extra inputs of the backward pass
     const void* d_o;

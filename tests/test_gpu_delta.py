@@ -488,3 +488,36 @@ def test_waits_that_run_out_are_reported(monkeypatch, Hv, T, D, backward, skip):
     got = run(x, workspace=ws)
     assert la.la_query_device_status(ws) == la.LA_OK
     assert all(_same(got[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("T", [12, 70, 200])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_growth_after_a_forgotten_state(T, D, dtype):
+    """Positive log_alpha behind a token that forgets: nothing of the state before it comes back.
+    Without writes the state stays exactly 0."""
+    x = delta_inputs(1, 2, 2, T, D, dtype, seed=100 + T)
+    x["log_alpha"][:, 0, 5] = -float("inf")
+    x["log_alpha"][:, 1, 5] = -105.0
+    x["log_alpha"][:, :, 6], x["log_alpha"][:, :, 7] = 50.0, 30.0
+    x["beta"][:, :, 5:] = 0.0
+    o, end = _forward(x)
+    assert (o[:, :, 5:] == 0).all() and (end == 0).all()
+    ro, _ = delta_ref(**to64(x))
+    check(o[:, :, :5], ro[:, :, :5], delta_bound(T), "o")
+
+
+@pytest.mark.parametrize("T,D", [(70, 64), (130, 128), (40, 48)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_no_gradient_where_the_decay_is_zero(T, D, dtype):
+    """dlog_alpha is exactly 0 wherever exp(log_alpha) is 0 in float32, not only at -inf."""
+    x = delta_inputs(2, 2, 4, T, D, dtype, seed=110 + T)
+    at = torch.arange(3, T, 7)
+    for i, value in enumerate((-104.0, -104.5, -110.0, -128.0, -1e4, -float("inf"))):
+        x["log_alpha"][:, :, at[i::6]] = value
+    assert (torch.exp(x["log_alpha"][:, :, at]) == 0).all()
+    got = _backward(x)
+    assert (got["log_alpha"][:, :, at] == 0).all()
+    y = {**x, "log_alpha": x["log_alpha"].clamp(min=-2000.0)}
+    y["log_alpha"] = torch.where(y["log_alpha"] <= -104.0, -2000.0, y["log_alpha"])
+    check_grads(got, delta_grads_ref(y), y, 4 * delta_bound(T))
