@@ -163,6 +163,8 @@ def _space(workspace, need: int, like: torch.Tensor):
 def _rows(t, name: str, shape, dtype, device):
     """The strides of [..., D] rows, which are contiguous themselves.  The stride of an axis of
     one element is never taken; torch may report any value for it."""
+    if t is None:
+        raise ValueError(f"{name} is required")
     s = t.stride()
     if t.shape != shape or t.dtype is not dtype or t.get_device() != device or \
             (s[-1] != 1 and shape[-1] != 1):
@@ -190,6 +192,8 @@ def _inputs(q, k, v, log_alpha, beta, k_scale, q_scale, state_in, lengths, devic
     dtype = q.dtype
     code = _dtype_code(q)
     gates, f32 = vshape[:-1], torch.float32
+    if log_alpha is None or beta is None:
+        raise ValueError(f"{'beta' if beta is None else 'log_alpha'} is required")
     qs = _rows(q, "q", shape, dtype, device)
     ks = _rows(k, "k", shape, dtype, device)
     vs = _rows(v, "v", (B, Hv, T, D) if len(shape) == 4 else (B, Hv, D), dtype, device)
@@ -327,6 +331,8 @@ def la_add_rms_norm_fp8(x, residual, weight, eps: float = 1e-6, group: int = 128
         done = _elsewhere(stream, la_add_rms_norm_fp8, x, residual, weight, eps, group, h, y, scale)
         if done is not NotImplemented:
             return done
+    if weight is None:
+        raise ValueError("weight is required")
     shape, dtype = x.shape, x.dtype
     N = shape[-1]
     dt = _dtype_code(x)
@@ -371,6 +377,8 @@ def la_add_rms_norm_backward(dy, h, weight, dh=None, eps: float = 1e-6, dx=None,
                           need_dweight, workspace)
         if done is not NotImplemented:
             return done
+    if weight is None:
+        raise ValueError("weight is required")
     shape, dtype = h.shape, h.dtype
     N = shape[-1]
     dt = _dtype_code(h)

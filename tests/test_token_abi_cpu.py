@@ -144,3 +144,17 @@ def test_workspaces_of_a_call():
     for view in (torch.zeros(1, dtype=torch.uint8).expand(512), whole[::2]):
         with pytest.raises(ValueError, match="workspace"):
             space(view, 256, like)
+
+
+def test_missing_tensors_are_named():
+    rows, gates = torch.zeros(1, 1, 4, 64), torch.zeros(1, 1, 4)
+    inputs = lambda k=rows, log_alpha=gates, beta=gates: la.token_ops._inputs(
+        rows, k, rows, log_alpha, beta, 1.0, 1.0, None, None, -1)
+    assert inputs()[1] == la.LA_F32
+    for name in ("k", "log_alpha", "beta"):
+        with pytest.raises(ValueError, match=name + " is required"):
+            inputs(**{name: None})
+    for call in (lambda: la.la_add_rms_norm_fp8(rows, None, None),
+                 lambda: la.la_add_rms_norm_backward(rows, rows, None)):
+        with pytest.raises(ValueError, match="weight is required"):
+            call()
