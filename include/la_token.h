@@ -26,7 +26,10 @@
  * exponential is 0 in float32).  Positive log_alpha is computed as written and may
  * overflow, in the chunked kernels where the sum of neighbouring ones passes 88.  NaN and infinities spread to later tokens as the recurrence
  * carries them, and in the chunked kernels also to the earlier tokens of the
- * same 64; rows behind a sequence's length never matter.
+ * same 64; rows behind a sequence's length never matter.  Forgetting is a product
+ * with 0: a state that holds NaN or infinity stays NaN in the value columns that hold
+ * it (and in no others), on every path.  To start anew from one, pass zeros or
+ * state_in = NULL.
  */
 #ifndef LA_TOKEN_H
 #define LA_TOKEN_H

@@ -521,3 +521,29 @@ def test_no_gradient_where_the_decay_is_zero(T, D, dtype):
     y = {**x, "log_alpha": x["log_alpha"].clamp(min=-2000.0)}
     y["log_alpha"] = torch.where(y["log_alpha"] <= -104.0, -2000.0, y["log_alpha"])
     check_grads(got, delta_grads_ref(y), y, 4 * delta_bound(T))
+
+
+@pytest.mark.parametrize("T,D,Hv", [(1, 64, 2), (10, 64, 2), (150, 64, 2), (150, 128, 2),
+                                    (10, 144, 2), (1600, 64, 1)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_forgetting_does_not_clean_a_state(T, D, Hv, dtype):
+    """A forgetting token multiplies the state by 0, so what is not finite in it stays, as NaN,
+    in its value column and in no other; on every path alike."""
+    x = delta_inputs(1, 1, Hv, T, D, dtype, seed=120 + T)
+    x["log_alpha"][:, :, 0] = -float("inf")
+    clean, clean_end = _forward(x)
+    assert torch.isfinite(clean).all() and torch.isfinite(clean_end).all()
+    x["state"][:, :, 2, 3] = float("inf")
+    x["state"][:, :, 1, 17] = float("nan")
+    runs = [_forward(x)]
+    if T == 1:
+        a = [t[:, :, 0] for t in _args(x)]
+        a[3], a[4] = a[3].contiguous(), a[4].contiguous()
+        end = torch.empty_like(clean_end)
+        o = la.la_gated_delta_step(*a, x["state"], state_out=end, **_kw(x))
+        runs.append((o[:, :, None], end))
+    rest = [c for c in range(D) if c not in (3, 17)]
+    for o, end in runs:
+        for c in (3, 17):
+            assert torch.isnan(o[..., c]).all() and torch.isnan(end[..., c]).all()
+        assert _same(o[..., rest], clean[..., rest]) and _same(end[..., rest], clean_end[..., rest])
