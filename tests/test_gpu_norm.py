@@ -283,3 +283,24 @@ def test_backward_of_large_and_small_rows(N, dtype, size, eps):
     h = (h.float() * size).to(dtype)
     dx, dw = la.la_add_rms_norm_backward(dy, h, w, eps=eps)
     _check_backward(dy, h, w, None, eps, dx, dw, steps=3 + 40)
+
+
+# a vector, two or four a thread; rows from the ring in shared memory or from memory; a
+# warp a row and several
+@pytest.mark.parametrize("rows,N,dtype", [
+    (7001, 144, BF16), (6001, 1008, BF16), (6001, 1008, F32), (4003, 2240, BF16),
+    (3001, 2240, F32), (2003, 4800, F32), (1501, 8192, BF16), (1501, 8192, F32),
+    (1201, 8448, BF16), (1201, 8448, F32), (1000, 16384, BF16), (1000, 16384, F32)])
+def test_backward_of_many_rows(rows, N, dtype):
+    """Several rows a block: at most 20 blocks an SM of 148, 2960, and no more than about 640
+    threads an SM from 32 a row on."""
+    threads = -(-N // 8 // (1 if N <= 1024 else 2 if N <= 8192 else 4) // 32) * 32
+    assert rows > 148 * max(1, 640 // threads)
+    h, dy, w = _inputs(rows, N, dtype, seed=N + 3)
+    dh = _inputs(rows, N, dtype, seed=N + 4, residual=False)[0]
+    # a sum over the rows: those of a block (at least 148 blocks), then of the blocks' sums
+    # (at most 2960) up to 93 by one of 32 threads, and 10 joins
+    steps = -(-rows // 148) + 93 + 10
+    for extra in (dh, None):
+        dx, dw = la.la_add_rms_norm_backward(dy, h, w, dh=extra, eps=EPS)
+        _check_backward(dy, h, w, extra, EPS, dx, dw, steps)
