@@ -64,9 +64,11 @@ typedef struct la_delta {
 
 /*
  * Forward pass over T tokens.
- * o         out: [B, Hv, T, D] of dtype dt with strides o_stride (rows must not
- *                overlap each other or an input); rows behind a sequence's
- *                length are left as they were.
+ * o         out: [B, Hv, T, D] of dtype dt with strides o_stride.  Rows must not
+ *                overlap each other, nor may what lies from o's first to its last
+ *                element overlap what lies from an input's first to its last (o between
+ *                an input's rows is refused).  Rows behind a sequence's length are left
+ *                as they were.
  * state_out out: [B, Hv, D, D] f32, the state after the sequence's last token,
  *                or NULL.  state_out == in->state_in is allowed.
  * T == 0 writes the initial state to state_out and nothing else.
@@ -131,8 +133,11 @@ LA_API const char* la_delta_plan(int backward, la_dtype dt, int B, int Hk, int H
  *     h = round_dt(x + residual)                   (h = x without a residual)
  *     y = h / sqrt(mean(h^2) + eps) * weight
  *     scale = max |y| / 448 over each group of columns (1 where that is 0 in float32)
- *     y8 = e4m3(y / scale), rounded to nearest even
- * h is normalised as it is stored, so that the backward pass sees the same h.
+ *     y8 = e4m3(y / scale)
+ * h is normalised as it is stored, so that the backward pass sees the same h.  The
+ * quotient is y times the float32 reciprocal of scale (off by 1.5 roundings of float32
+ * in place of half of one) and is rounded to nearest even, so that a value within those
+ * of the middle between two e4m3 numbers may go to the other one.
  * group = 128: a scale for each 128 columns (the last group may be shorter);
  * group = 0: one scale for the row.  A row that holds NaN or infinity gives
  * NaN in what it reaches.  The squares are summed in float32: a row whose sum of

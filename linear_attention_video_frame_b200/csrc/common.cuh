@@ -91,7 +91,9 @@ __device__ __forceinline__ void store_elem(void* p, size_t i, float x, int bf16)
 
 // Per-device facts (devinfo.cu).  A process may drive several GPUs, so
 // everything that belongs to a device is cached per device.
-constexpr int kDefaultSmCount = 148;   // B200; used only when no device is visible
+// SMs of a B200: where no device is visible, and where a plan fixes the size of a workspace,
+// which must not depend on the device (Segments::plan, norm_backward_blocks).
+constexpr int kDefaultSmCount = 148;
 int current_device();                   // current device, or -1
 int device_sm_count();                  // SMs of the current device (cached per device)
 // Opt `kernel` in to at least `bytes` of dynamic shared memory on the

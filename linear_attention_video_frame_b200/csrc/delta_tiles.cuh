@@ -25,7 +25,9 @@ struct Segments {
     int count, chunks;           // of a head; of a segment
 
     // Chunk times (2 to 4 us) of the passes: rounds of jobs over the SMs, one job each;
-    // the second pass's start costs about three more, a join (10 to 23 us) six.
+    // the second pass's start costs about three more, a join (10 to 23 us) six.  For the
+    // SMs of a B200, whatever the device: a workspace's size follows from the plan, and its
+    // owner asks for it by shape alone.
     static Segments plan(int backward, int heads, int chunks) {
         auto rounds = [](long long jobs) {
             return (double)((jobs + kDefaultSmCount - 1) / kDefaultSmCount);

@@ -548,7 +548,7 @@ static int backward_blocks(long long rows, int N, int elem) {
     const long long most = (long long)kDefaultSmCount * each;
     return (int)(rows < most ? rows : most);
 }
-// The most of both types: the workspace's size does not depend on the type.
+// The most of both types: the workspace's size depends on neither the type nor the device.
 int norm_backward_blocks(long long rows, int N) {
     const int a = backward_blocks(rows, N, 2), b = backward_blocks(rows, N, 4);
     return a > b ? a : b;

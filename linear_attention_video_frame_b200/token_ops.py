@@ -9,6 +9,9 @@ as the D values of a row are contiguous, for example ``[B, T, H, D]``
 transposed; log_alpha, beta ``[B, Hv, T]`` and states ``[B, Hv, D, D]`` are
 contiguous float32; lengths ``[B]`` is int32 or None.
 
+Autograd does not see these calls: results carry no graph, and the backward passes
+are functions of their own.
+
 ``stream`` is a torch stream or the address of a CUDA stream (default: the current
 one).  Inputs, and outputs that are given, have to be ready on it; a call's new
 outputs are made on it and may be used on the current stream once that waits for it.
