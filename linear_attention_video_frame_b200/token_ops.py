@@ -129,7 +129,10 @@ def _elsewhere(stream, call, *args, **kw):
     is where the caller uses them, so their memory waits for it as well."""
     here = torch.cuda.current_stream()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), here.device)
+        address = int(getattr(stream, "cuda_stream", stream))
+        # 0, and CUDA's name for it, 1, are no addresses to ExternalStream
+        stream = torch.cuda.ExternalStream(address, here.device) if address > 1 else \
+            torch.cuda.default_stream(here.device)
     if stream.cuda_stream == here.cuda_stream:
         return NotImplemented
     with torch.cuda.stream(stream):

@@ -547,3 +547,21 @@ def test_forgetting_does_not_clean_a_state(T, D, Hv, dtype):
         for c in (3, 17):
             assert torch.isnan(o[..., c]).all() and torch.isnan(end[..., c]).all()
         assert _same(o[..., rest], clean[..., rest]) and _same(end[..., rest], clean_end[..., rest])
+
+
+@pytest.mark.parametrize("address", [0, 1])
+def test_the_default_stream_by_its_address(address):
+    """From another current stream: the calls wait for what the default stream has to do."""
+    x = delta_inputs(1, 2, 2, 200, 64, seed=94)
+    want = _forward(x)[0]
+    o, early = torch.full_like(x["v"], 7.0), torch.empty_like(x["v"])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _hold()                                     # the default stream
+    with torch.cuda.stream(side):
+        la.la_gated_delta_rule(*_args(x), state_in=x["state"], o=o, **_kw(x), stream=address)
+        early.copy_(o)
+        p = la.la_gated_delta_rule(*_args(x), state_in=x["state"], **_kw(x), stream=address)
+    torch.cuda.synchronize()
+    assert (early == 7.0).all()
+    assert _same(o, want) and _same(p, want)
