@@ -12,8 +12,8 @@
 //
 // The chain of products and register work bounds it, not its bytes: 2300 cycles of
 // products and as many of register work depend on one another, 4800 cycles a chunk in
-// all, with outputs 5300 to 6000 (80 heads of 128, 32 chunks: 118 us, DRAM at 24 % of
-// its peak).
+// all, with outputs 5300 to 6000 (80 heads of 128, 32 chunks: 120 to 124 us, DRAM at
+// 25 % of its peak).
 #include "delta_tc.cuh"
 
 namespace la {

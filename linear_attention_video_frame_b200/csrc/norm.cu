@@ -6,7 +6,8 @@
 // holds VPT vectors of 8 neighbouring columns (16 bytes of bf16); 16
 // neighbouring lanes then hold the 128 columns of one scale group, so a
 // group's maximum takes four shuffles and no shared memory.  28160 rows of 2560 in
-// bf16 with a residual: 90 us, 5.6 TB/s; backward, 8192 rows of 2560: 37 us, 4.5 TB/s.
+// bf16 with a residual: 90 us, 5.6 TB/s (float32: 148 us, 6.4); backward, 8192 rows of 2560:
+// 37 us, 4.5 TB/s (float32: 76 us, 4.4).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
